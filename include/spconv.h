@@ -491,6 +491,189 @@ SPCONV_API spconv_status_t spconv_subdivide(const int32_t* coords, int64_t n, co
                                             spconv_dtype_t dtype, const void* x, int32_t channels,
                                             int32_t* coords_out, void* x_out, void* stream);
 
+/*
+ * ------------------------------------------------- operators on feature rows
+ * What the transformer blocks around the sparse convolutions do to the feature
+ * rows [n, channels] of an active-voxel set before their attention: the norm with
+ * the residual's addition, the projection by quantised weights, and the rotary
+ * positions.  The pixal3d_mrp_mlx README and the trellis2mlx README list the DiT
+ * blocks with their q/k RMS norm and rotary embedding; the trellis2-mlx-8bit model
+ * card keeps block matrices in affine 4- and 8-bit groups.
+ *
+ * Every call below only validates on the host and launches on `stream`, on the
+ * current CUDA device: no synchronisation, no allocation, nothing kept between
+ * calls (so each can be captured into a CUDA graph).  Errors: SPCONV_ERR_INVALID_ARG
+ * (null, misaligned or overlapping buffers, sizes out of range),
+ * SPCONV_ERR_UNSUPPORTED, SPCONV_ERR_CUDA.
+ */
+
+#define SPCONV_NORM_MAX_CHANNELS 65536
+#define SPCONV_ROPE_MAX_HEAD_DIM 256
+#define SPCONV_W4_MAX_ROWS 32
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *
+ *   h = x + residual,  rstd = (mean over channels of h^2 + eps)^(-1/2),
+ *   out = h * rstd * weight.
+ *
+ * All of it is fp32; out and sum_out are each rounded once (out from the unrounded
+ * h).  A row with an infinity or a NaN gives what the formula gives in fp32.
+ *
+ *   x         device [n, channels] of dtype, 0 <= n < 2^31, 1 <= channels <=
+ *             SPCONV_NORM_MAX_CHANNELS.
+ *   residual  device [n, channels] of dtype, or NULL.
+ *   weight    device [channels] of dtype, or NULL (ones).
+ *   eps       finite, >= 0.
+ *   sum_out   device [n, channels] of dtype, or NULL: receives h.  Needs a residual;
+ *             may be residual or x itself, and must not overlap them otherwise.
+ *   out       device [n, channels] of dtype; overlaps no other buffer.
+ *   rstd      device fp32 [n], or NULL: receives rstd, which the gradient reads.
+ */
+SPCONV_API spconv_status_t spconv_rms_norm(spconv_dtype_t dtype, const void* x, const void* residual,
+                                           const void* weight, int64_t n, int32_t channels, float eps, void* sum_out,
+                                           void* out, float* rstd, void* stream);
+
+/*
+ * spconv_rms_norm with the result in 8 bits and a scale per row:
+ *
+ *   y = h * rstd * weight,  scale = max(max over channels of |y| / 448, 2^-126),
+ *   q = y / scale rounded to e4m3 (4 exponent, 3 mantissa bits; nearest even).
+ *
+ * y is not rounded in between.  A row whose y has a NaN has a NaN scale and NaN codes.
+ *
+ *   q         device bytes [n, channels] (e4m3), scale device fp32 [n].
+ */
+SPCONV_API spconv_status_t spconv_rms_norm_q8(spconv_dtype_t dtype, const void* x, const void* residual,
+                                              const void* weight, int64_t n, int32_t channels, float eps, void* sum_out,
+                                              uint8_t* q, float* scale, void* stream);
+
+/* Bytes of device workspace that spconv_rms_norm_backward needs for dweight. */
+SPCONV_API spconv_status_t spconv_rms_norm_workspace(int64_t n, int32_t channels, int64_t* bytes);
+
+/*
+ * Gradient of spconv_rms_norm.  With xh = h * rstd and g = dy * weight:
+ *
+ *   dx = rstd * (g - xh * mean over channels of (g * xh)) (+ dsum),
+ *   dweight = sum over rows of dy * xh.
+ *
+ * dx is the gradient of x and of the residual alike.
+ *
+ *   dy, h     device [n, channels] of dtype; h is sum_out, or x where the forward
+ *             had no residual.
+ *   weight    device [channels] of dtype, or NULL (ones).
+ *   rstd      device fp32 [n], as the forward wrote it.
+ *   dsum      device [n, channels] of dtype, or NULL: the gradient that reaches
+ *             sum_out by other ways, added in fp32.
+ *   dx        device [n, channels] of dtype; may be dsum itself.
+ *   dweight   device fp32 [channels], or NULL (not computed; the workspace is then
+ *             not used).  Written, not added to; zeros for n = 0.  The rows are added
+ *             in an order that depends on n and channels alone: the same inputs give
+ *             the same bits.
+ *   workspace device, spconv_rms_norm_workspace() bytes.  Its contents before and
+ *             after mean nothing; calls that may overlap in time need one each.
+ */
+SPCONV_API spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, const void* h,
+                                                    const void* weight, const float* rstd, const void* dsum, int64_t n,
+                                                    int32_t channels, void* dx, float* dweight, void* workspace,
+                                                    void* stream);
+
+/*
+ * Rotary positions with several axes.  Pair j of each head of voxel i is turned by
+ * the angle t = freqs[j] * coords[i, 1 + axes[j]]:
+ *
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t).
+ *
+ * SPCONV_ROPE_INTERLEAVED: pair j is the elements (2j, 2j + 1) of the head;
+ * SPCONV_ROPE_HALVES: (j, j + head_dim / 2).  The columns of coords are (b, x, y, z)
+ * for voxels; rows of a video carry (b, time, height, width).
+ */
+typedef enum { SPCONV_ROPE_INTERLEAVED = 0, SPCONV_ROPE_HALVES = 1 } spconv_rope_layout_t;
+typedef struct spconv_rope_s* spconv_rope_t; /* opaque, host memory, owned by the library */
+
+/*
+ * Prepare the turns of a head.
+ *
+ *   head_dim  even, in [2, SPCONV_ROPE_MAX_HEAD_DIM].
+ *   freqs     host double [head_dim / 2], radians per unit of the coordinate, finite.
+ *   axes      host int32 [head_dim / 2]: 0, 1 or 2 (columns 1, 2, 3 of coords), or
+ *             -1: the pair does not turn.
+ *             Both NULL: P = head_dim / 2 / 3 pairs an axis, in the order x, y, z,
+ *             with base^(-j / P), j = 0 .. P - 1; the pairs left over do not turn.
+ *   base      positive; only read where freqs is NULL.
+ *   out       receives the handle on success.  It holds no device memory and may be
+ *             used on any device and stream.
+ */
+SPCONV_API spconv_status_t spconv_rope_create(int32_t head_dim, spconv_rope_layout_t layout, double base,
+                                              const double* freqs, const int32_t* axes, spconv_rope_t* out);
+
+/* Release a rope.  The calls made with it may still run: they hold their own copy.
+ * NULL is accepted and ignored. */
+SPCONV_API spconv_status_t spconv_rope_free(spconv_rope_t rope);
+
+/*
+ * Turn the heads of n voxels.
+ *
+ *   coords    device int32 [n, 4], 16-byte aligned; any 32-bit value.  Angles are
+ *             exact to 2^-32 of a turn at every coordinate.
+ *   x         device, aligned to the element: element e of head k of voxel i is at
+ *             x[i * x_row + k * x_head + e], so x may be a part of a packed projection.
+ *             Strides in elements, in [head_dim, 2^40] (x_row is not read for n = 1,
+ *             x_head not for heads = 1).  16-byte aligned buffers whose strides are
+ *             multiples of 16 bytes run faster.
+ *   heads     in [1, 65535].
+ *   out       as x, with its own strides; rows and heads of out share no elements.
+ *             May be x itself with the same strides; must not overlap it otherwise.
+ *   inverse   nonzero: turn by -t.  That is also the gradient: dx from dout.
+ */
+SPCONV_API spconv_status_t spconv_rope_apply(spconv_rope_t rope, spconv_dtype_t dtype, const int32_t* coords, int64_t n,
+                                             const void* x, int32_t heads, int64_t x_row, int64_t x_head, void* out,
+                                             int64_t out_row, int64_t out_head, int32_t inverse, void* stream);
+
+/*
+ * 4-bit weights in groups.  A matrix [cin, cout] (the weights of a map of kernel
+ * size 1) is held as
+ *
+ *   packed    device uint32 [cout, cin / 8]: bits 4e .. 4e + 3 of word [o, m] are the
+ *             code q of input channel 8m + e,
+ *   scales, offsets  device [cout, cin / group] of dtype:
+ *             w[k, o] = scales[o, k / group] * q + offsets[o, k / group],
+ *
+ * the layout in which the trellis2-mlx-8bit model card's affine groups are stored.
+ * group is 32, 64 or 128; cin is a multiple of group, cin and cout at most 2^20.
+ *
+ * spconv_w4_quantize: from w, device [cin, cout] of dtype, finite.  offset = the
+ * group's minimum, scale = (maximum - minimum) / 15, both rounded to dtype; q is the
+ * nearest code for the rounded pair (0 where the scale is 0).
+ */
+SPCONV_API spconv_status_t spconv_w4_quantize(spconv_dtype_t dtype, const void* w, int32_t cin, int32_t cout,
+                                              int32_t group, uint32_t* packed, void* scales, void* offsets,
+                                              void* stream);
+
+/* The weights back: w, device [cin, cout] of dtype, each rounded once.  With a map of
+ * kernel size 1 this serves row counts that spconv_linear_w4 does not take. */
+SPCONV_API spconv_status_t spconv_w4_dequantize(spconv_dtype_t dtype, const uint32_t* packed, const void* scales,
+                                                const void* offsets, int32_t cin, int32_t cout, int32_t group, void* w,
+                                                void* stream);
+
+/*
+ * The linear layer on 4-bit weights, for few rows:
+ *
+ *   out[i, o] = bias[o] + x_scale[i] * sum over k of w[k, o] * x[i, k],
+ *
+ * with w as above, not rounded; sums in fp32, one rounding.
+ *
+ *   x         device [n, cin] of dtype, or, where x_scale is given, e4m3 bytes.
+ *   x_scale   device fp32 [n] (as spconv_rms_norm_q8 writes it), or NULL.
+ *   n         0 <= n <= SPCONV_W4_MAX_ROWS (more: SPCONV_ERR_UNSUPPORTED).
+ *   bias      device [cout] of dtype, or NULL.
+ *   out       device [n, cout] of dtype; overlaps no other buffer.
+ */
+SPCONV_API spconv_status_t spconv_linear_w4(spconv_dtype_t dtype, const void* x, const float* x_scale, int64_t n,
+                                            int32_t cin, const uint32_t* packed, const void* scales,
+                                            const void* offsets, int32_t group, const void* bias, void* out,
+                                            int32_t cout, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

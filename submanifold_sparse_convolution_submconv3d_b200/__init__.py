@@ -14,9 +14,15 @@ The functions carry the C names:
 * ``spconv_downsample_build(coords, extent, factor=2)`` -> ``Downsample``;
   ``spconv_downsample_amax(ds, x)``, ``spconv_upsample(ds, x_coarse)``
 * ``spconv_subdivide(coords, extent, x=None)`` -> ``(coords_out, x_out)``
+* ``spconv_rms_norm(x, weight, residual=None)`` -> ``out`` or ``(out, sum)``; ``spconv_rms_norm_q8`` ->
+  ``(q, scale)`` or ``(q, scale, sum)``; ``spconv_rms_norm_backward(dy, h, weight, rstd)`` -> ``(dx, dweight)``
+* ``spconv_rope_create(head_dim)`` -> ``Rope``; ``spconv_rope_apply(rope, coords, x, inverse=False)`` -> ``out``
+* ``spconv_w4_quantize(w)`` -> ``(packed, scales, offsets)``; ``spconv_w4_dequantize``;
+  ``spconv_linear_w4(x, packed, scales, offsets, bias=None, x_scale=None)`` -> ``out``
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -28,6 +34,9 @@ LIB_PATH = os.path.join(_HERE, "libspconv_b200.so")
 OK, INVALID_ARG, UNSUPPORTED, COORD_RANGE, DUPLICATE, TABLE_FULL, OOM, CUDA_ERROR, TIMEOUT = range(9)
 MAP_DEFAULT, MAP_FLIP_KERNEL, MAP_SORTED_KEYS, MAP_HASH_TABLE, MAP_SHORT_TILES = 0, 1, 2, 4, 8
 ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05 = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_HALVES = 0, 1
+ROPE_LAYOUTS = {"interleaved": ROPE_INTERLEAVED, "halves": ROPE_HALVES}
+W4_MAX_ROWS = 32
 KERNEL_SIMT, KERNEL_TCGEN05, KERNEL_TCGEN05_GEMM = 0, 1, 2
 KERNEL_NAMES = ("simt", "tcgen05", "tcgen05_gemm")
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -38,7 +47,9 @@ EXPORTED = ("spconv_build_map", "spconv_subm_forward", "spconv_free", "spconv_ma
             "spconv_debug_set_tile_rows", "spconv_build_neighbor_map_noalloc", "spconv_map_launch_counts",
             "spconv_map_stats", "spconv_debug_set_ring_depths", "spconv_build_map_ex", "spconv_downsample_build",
             "spconv_downsample_info", "spconv_downsample_amax", "spconv_upsample", "spconv_downsample_free",
-            "spconv_subdivide", "spconv_subm_forward_ex")
+            "spconv_subdivide", "spconv_subm_forward_ex", "spconv_rms_norm", "spconv_rms_norm_q8",
+            "spconv_rms_norm_workspace", "spconv_rms_norm_backward", "spconv_rope_create", "spconv_rope_free",
+            "spconv_rope_apply", "spconv_w4_quantize", "spconv_w4_dequantize", "spconv_linear_w4")
 
 
 class _MapStats(ctypes.Structure):
@@ -90,13 +101,27 @@ def _load() -> ctypes.CDLL:
     lib.spconv_subdivide.argtypes = [vp, i64, vp, ctypes.c_int, vp, i32, vp, vp, vp]
     lib.spconv_subm_forward_ex.argtypes = [vp, ctypes.c_int, vp, i32, vp, vp, vp, i32, ctypes.POINTER(_Epilogue),
                                            ctypes.c_int, vp]
+    f32, fn = ctypes.c_float, ctypes.c_int
+    lib.spconv_rms_norm.argtypes = [fn, vp, vp, vp, i64, i32, f32, vp, vp, vp, vp]
+    lib.spconv_rms_norm_q8.argtypes = [fn, vp, vp, vp, i64, i32, f32, vp, vp, vp, vp]
+    lib.spconv_rms_norm_workspace.argtypes = [i64, i32, ctypes.POINTER(i64)]
+    lib.spconv_rms_norm_backward.argtypes = [fn, vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, vp]
+    lib.spconv_rope_create.argtypes = [i32, fn, ctypes.c_double, vp, vp, ctypes.POINTER(vp)]
+    lib.spconv_rope_free.argtypes = [vp]
+    lib.spconv_rope_apply.argtypes = [vp, fn, vp, i64, vp, i32, i64, i64, vp, i64, i64, i32, vp]
+    lib.spconv_w4_quantize.argtypes = [fn, vp, i32, i32, i32, vp, vp, vp, vp]
+    lib.spconv_w4_dequantize.argtypes = [fn, vp, vp, vp, i32, i32, i32, vp, vp]
+    lib.spconv_linear_w4.argtypes = [fn, vp, vp, i64, i32, vp, vp, vp, i32, vp, vp, i32, vp]
     lib.spconv_last_error.restype = ctypes.c_char_p
     for name in ("spconv_build_map", "spconv_subm_forward", "spconv_subm_forward_algo", "spconv_free",
                  "spconv_map_info", "spconv_map_check", "spconv_map_tile_rows", "spconv_debug_set_table_slots",
                  "spconv_debug_set_tile_rows", "spconv_build_neighbor_map_noalloc", "spconv_map_launch_counts",
                  "spconv_map_stats", "spconv_debug_set_ring_depths", "spconv_build_map_ex",
                  "spconv_downsample_build", "spconv_downsample_info", "spconv_downsample_amax", "spconv_upsample",
-                 "spconv_downsample_free", "spconv_subdivide", "spconv_subm_forward_ex"):
+                 "spconv_downsample_free", "spconv_subdivide", "spconv_subm_forward_ex", "spconv_rms_norm",
+                 "spconv_rms_norm_q8", "spconv_rms_norm_workspace", "spconv_rms_norm_backward", "spconv_rope_create",
+                 "spconv_rope_free", "spconv_rope_apply", "spconv_w4_quantize", "spconv_w4_dequantize",
+                 "spconv_linear_w4"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -427,6 +452,307 @@ def spconv_subdivide(coords: torch.Tensor, extent, x: torch.Tensor | None = None
     return coords_out, x_out
 
 
+# ------------------------------------------------------------ operators on feature rows
+# One token's row is a few microseconds of GPU work, so these calls keep the host side
+# short: they enter a device or stream context only where it is not current already.
+
+def _elsewhere(x: torch.Tensor, stream) -> bool:
+    return stream is not None or x.device.index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Make ``stream`` (None: the device's current stream) the current one, so that the
+    results and temporaries of a call are allocated and written in its order."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _in(t: torch.Tensor) -> torch.Tensor:
+    """An input as the library reads it: contiguous, on a 16-byte boundary."""
+    t = t.contiguous()
+    return t if t.data_ptr() & 15 == 0 else t.clone()
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _like(t, shape, dtype, device, what: str) -> None:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} must be a {str(dtype)[6:]} tensor {list(shape)} on {device}; got "
+                         f"{str(t.dtype)[6:]} {list(t.shape)} on {t.device}")
+
+
+def _out(t, shape, dtype, device, what: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _like(t, shape, dtype, device, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t
+
+
+def _norm_rows(x, weight, what: str) -> None:
+    if x.dtype not in _DTYPES or not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{what} must be a float32 or bfloat16 CUDA tensor [N, C]")
+    if weight is not None:
+        _like(weight, (x.shape[1],), x.dtype, x.device, "weight")
+
+
+def spconv_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                    eps: float = 1e-6, out: torch.Tensor | None = None, sum_out: torch.Tensor | None = None,
+                    rstd: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of rows x [N, C], with the residual's addition: returns
+    ``out``, or ``(out, sum)`` with sum = x + residual where a residual is given.
+    ``sum_out`` may be ``residual`` or ``x`` itself; ``rstd``, a float32 CUDA tensor [N],
+    receives what ``spconv_rms_norm_backward`` reads."""
+    _require()
+    _norm_rows(x, weight, "x")
+    if _elsewhere(x, stream):
+        with _on(x.device, stream):
+            return spconv_rms_norm(x, weight, residual, eps, out, sum_out, rstd)
+    if residual is not None:
+        _like(residual, x.shape, x.dtype, x.device, "residual")
+        sum_out = _out(sum_out, x.shape, x.dtype, x.device, "sum_out")
+        residual = _in(residual)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    if rstd is not None:
+        _out(rstd, (x.shape[0],), torch.float32, x.device, "rstd")
+    out = _out(out, x.shape, x.dtype, x.device, "out")
+    x = _in(x)
+    weight = None if weight is None else _in(weight)
+    _check(lib.spconv_rms_norm(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), x.shape[0], x.shape[1],
+                               eps, _ptr(sum_out), out.data_ptr(), _ptr(rstd), _stream(None)))
+    return out if residual is None else (out, sum_out)
+
+
+def spconv_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                       eps: float = 1e-6, out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                       sum_out: torch.Tensor | None = None, stream=None):
+    """``spconv_rms_norm`` with the result in 8 bits: returns ``(q, scale)`` or ``(q,
+    scale, sum)``, q float8_e4m3fn [N, C] and scale float32 [N], the norm being about
+    q * scale."""
+    _require()
+    _norm_rows(x, weight, "x")
+    if _elsewhere(x, stream):
+        with _on(x.device, stream):
+            return spconv_rms_norm_q8(x, weight, residual, eps, out, scale, sum_out)
+    if residual is not None:
+        _like(residual, x.shape, x.dtype, x.device, "residual")
+        sum_out = _out(sum_out, x.shape, x.dtype, x.device, "sum_out")
+        residual = _in(residual)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    out = _out(out, x.shape, torch.float8_e4m3fn, x.device, "out")
+    scale = _out(scale, (x.shape[0],), torch.float32, x.device, "scale")
+    x = _in(x)
+    weight = None if weight is None else _in(weight)
+    _check(lib.spconv_rms_norm_q8(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), x.shape[0], x.shape[1],
+                                  eps, _ptr(sum_out), out.data_ptr(), scale.data_ptr(), _stream(None)))
+    return (out, scale) if residual is None else (out, scale, sum_out)
+
+
+def spconv_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
+                             dsum: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                             weight_grad: bool = True, stream=None):
+    """Gradient of ``spconv_rms_norm``: returns ``(dx, dweight)``.  h is the sum (or x
+    where there was no residual); dx is the gradient of x and of the residual, with
+    ``dsum``, the gradient that reaches the sum by other ways, added (dx may be dsum
+    itself).  dweight is float32 [C], or None without a weight or with weight_grad False."""
+    _require()
+    _norm_rows(h, weight, "h")
+    if _elsewhere(h, stream):
+        with _on(h.device, stream):
+            return spconv_rms_norm_backward(dy, h, weight, rstd, dsum, dx, weight_grad)
+    n, c = h.shape
+    _like(dy, h.shape, h.dtype, h.device, "dy")
+    _like(rstd, (n,), torch.float32, h.device, "rstd")
+    if dsum is not None:
+        _like(dsum, h.shape, h.dtype, h.device, "dsum")
+        dsum = _in(dsum)
+    dx = _out(dx, h.shape, h.dtype, h.device, "dx")
+    dweight = workspace = None
+    if weight is not None:
+        weight = _in(weight)
+        if weight_grad:
+            size = ctypes.c_int64()
+            _check(lib.spconv_rms_norm_workspace(n, c, ctypes.byref(size)))
+            workspace = torch.empty(max(size.value, 16), dtype=torch.uint8, device=h.device)
+            dweight = torch.empty(c, dtype=torch.float32, device=h.device)
+    dy, h, rstd = _in(dy), _in(h), _in(rstd)
+    _check(lib.spconv_rms_norm_backward(_DTYPES[h.dtype], dy.data_ptr(), h.data_ptr(), _ptr(weight), rstd.data_ptr(),
+                                        _ptr(dsum), n, c, dx.data_ptr(), _ptr(dweight), _ptr(workspace),
+                                        _stream(None)))
+    return dx, dweight
+
+
+class Rope:
+    """Owns a rope handle (spconv_rope_create): the turns of a head's pairs.  It holds
+    no device memory and serves every device and stream."""
+
+    def __init__(self, handle: int, head_dim: int):
+        self.handle = handle
+        self.head_dim = head_dim
+
+    def free(self) -> None:
+        if self.handle:
+            lib.spconv_rope_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def spconv_rope_create(head_dim: int, layout: str = "interleaved", base: float = 10000.0, freqs=None,
+                       axes=None) -> Rope:
+    """Rotary positions of heads of ``head_dim`` elements.  ``layout``: "interleaved"
+    pairs (2j, 2j + 1), "halves" pairs (j, j + head_dim / 2).  ``freqs`` and ``axes``,
+    sequences of head_dim / 2 numbers, give each pair's radians per unit and its
+    coordinate (0, 1, 2 = x, y, z; -1 = the pair does not turn); without them every axis
+    has head_dim // 6 pairs with the ladder base^(-j / (head_dim // 6))."""
+    _require()
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    if (freqs is None) != (axes is None):
+        raise ValueError("freqs and axes are given together or not at all")
+    pairs = int(head_dim) // 2
+    if freqs is not None:
+        freqs, axes = [float(f) for f in freqs], [int(a) for a in axes]
+        if len(freqs) != pairs or len(axes) != pairs:
+            raise ValueError(f"freqs and axes must have head_dim / 2 = {pairs} entries")
+        freqs, axes = (ctypes.c_double * pairs)(*freqs), (ctypes.c_int32 * pairs)(*axes)
+    handle = ctypes.c_void_p()
+    _check(lib.spconv_rope_create(int(head_dim), ROPE_LAYOUTS[layout], float(base), freqs, axes, ctypes.byref(handle)))
+    return Rope(handle.value, int(head_dim))
+
+
+def spconv_rope_free(rope: Rope) -> None:
+    rope.free()
+
+
+def spconv_rope_apply(rope: Rope, coords: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None,
+                      inverse: bool = False, stream=None) -> torch.Tensor:
+    """Turn the heads x [N, heads, head_dim] by their voxels' coordinates (int32 [N, 4],
+    columns b, x, y, z).  x and out may be parts of a packed projection (any strides
+    whose heads are contiguous); out may be x itself.  ``inverse`` turns back, which is
+    also the gradient."""
+    _require()
+    if not rope.handle:
+        raise ValueError("the rope has been freed")
+    if x.dtype not in _DTYPES or not x.is_cuda or x.dim() != 3 or x.shape[2] != rope.head_dim or x.shape[1] < 1:
+        raise ValueError(f"x must be a float32 or bfloat16 CUDA tensor [N, heads, {rope.head_dim}]")
+    if coords.dtype != torch.int32 or coords.shape != (x.shape[0], 4) or coords.device != x.device:
+        raise ValueError(f"coords must be an int32 tensor [{x.shape[0]}, 4] on {x.device}")
+    if _elsewhere(x, stream):
+        with _on(x.device, stream):
+            return spconv_rope_apply(rope, coords, x, out, inverse)
+    n, heads, d = x.shape
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
+    else:
+        _like(out, x.shape, x.dtype, x.device, "out")
+        if out.stride(2) != 1:
+            raise ValueError("the heads of out must be contiguous")
+    if x.stride(2) != 1 or (n > 1 and x.stride(0) < d) or (heads > 1 and x.stride(1) < d):
+        x = x.contiguous()
+    coords = _in(coords)
+    _check(lib.spconv_rope_apply(rope.handle, _DTYPES[x.dtype], coords.data_ptr(), n, x.data_ptr(), heads, x.stride(0),
+                                 x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), bool(inverse),
+                                 _stream(None)))
+    return out
+
+
+def _w4_args(packed, scales, offsets) -> tuple[int, int, int]:
+    """(cin, cout, group) of 4-bit weights."""
+    if scales.dtype not in _DTYPES or not scales.is_cuda or scales.dim() != 2:
+        raise ValueError("scales must be a float32 or bfloat16 CUDA tensor [Cout, Cin / group]")
+    _like(offsets, scales.shape, scales.dtype, scales.device, "offsets")
+    if packed.dtype != torch.int32 or packed.device != scales.device or packed.dim() != 2 \
+            or packed.shape[0] != scales.shape[0] or scales.shape[1] < 1 or packed.shape[1] * 8 % scales.shape[1]:
+        raise ValueError(f"packed must be an int32 tensor [Cout, Cin / 8] on {scales.device}, with scales "
+                         f"[Cout, Cin / group]; got {list(packed.shape)} and {list(scales.shape)}")
+    cin = packed.shape[1] * 8
+    return cin, packed.shape[0], cin // scales.shape[1]
+
+
+def spconv_w4_quantize(w: torch.Tensor, group: int = 64, stream=None) -> tuple:
+    """4-bit weights of w [Cin, Cout] (or [1, Cin, Cout], as a layer of kernel size 1
+    has them): (packed int32 [Cout, Cin / 8], scales, offsets [Cout, Cin / group])."""
+    _require()
+    if w.dim() == 3 and w.shape[0] == 1:
+        w = w[0]
+    if w.dtype not in _DTYPES or not w.is_cuda or w.dim() != 2:
+        raise ValueError("w must be a float32 or bfloat16 CUDA tensor [Cin, Cout]")
+    cin, cout = w.shape
+    if group not in (32, 64, 128) or cin < group or cin % group or cout < 1:
+        raise ValueError(f"group must be 32, 64 or 128 and divide Cin = {cin}; Cout must be at least 1")
+    if _elsewhere(w, stream):
+        with _on(w.device, stream):
+            return spconv_w4_quantize(w, group)
+    w = _in(w)
+    packed = torch.empty((cout, cin // 8), dtype=torch.int32, device=w.device)
+    scales, offsets = (torch.empty((cout, cin // group), dtype=w.dtype, device=w.device) for _ in range(2))
+    _check(lib.spconv_w4_quantize(_DTYPES[w.dtype], w.data_ptr(), cin, cout, group, packed.data_ptr(),
+                                  scales.data_ptr(), offsets.data_ptr(), _stream(None)))
+    return packed, scales, offsets
+
+
+def spconv_w4_dequantize(packed: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The weights back, [1, Cin, Cout] of the scales' dtype: the weights of a layer of
+    kernel size 1, for more rows than ``spconv_linear_w4`` takes."""
+    _require()
+    cin, cout, group = _w4_args(packed, scales, offsets)
+    if _elsewhere(scales, stream):
+        with _on(scales.device, stream):
+            return spconv_w4_dequantize(packed, scales, offsets, out)
+    out = _out(out, (1, cin, cout), scales.dtype, scales.device, "out")
+    packed, scales, offsets = _in(packed), _in(scales), _in(offsets)
+    _check(lib.spconv_w4_dequantize(_DTYPES[scales.dtype], packed.data_ptr(), scales.data_ptr(), offsets.data_ptr(),
+                                    cin, cout, group, out.data_ptr(), _stream(None)))
+    return out
+
+
+def spconv_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
+                     bias: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Linear layer on 4-bit weights for up to W4_MAX_ROWS rows: x [N, Cin] of the
+    scales' dtype, or float8_e4m3fn with ``x_scale`` float32 [N] (as
+    ``spconv_rms_norm_q8`` returns them) -> out [N, Cout] of the scales' dtype."""
+    _require()
+    cin, cout, group = _w4_args(packed, scales, offsets)
+    dtype, device, n = scales.dtype, scales.device, x.shape[0] if x.dim() else 0
+    _like(x, (n, cin), dtype if x_scale is None else torch.float8_e4m3fn, device, "x")
+    if _elsewhere(scales, stream):
+        with _on(device, stream):
+            return spconv_linear_w4(x, packed, scales, offsets, bias, x_scale, out)
+    if x_scale is not None:
+        _like(x_scale, (n,), torch.float32, device, "x_scale")
+        x_scale = _in(x_scale)
+    if bias is not None:
+        _like(bias, (cout,), dtype, device, "bias")
+        bias = _in(bias)
+    out = _out(out, (n, cout), dtype, device, "out")
+    x, packed, scales, offsets = _in(x), _in(packed), _in(scales), _in(offsets)
+    _check(lib.spconv_linear_w4(_DTYPES[dtype], x.data_ptr(), _ptr(x_scale), n, cin, packed.data_ptr(),
+                                scales.data_ptr(), offsets.data_ptr(), group, _ptr(bias), out.data_ptr(), cout,
+                                _stream(None)))
+    return out
+
+
 def spconv_debug_set_table_slots(slots: int) -> None:
     _require()
     _check(lib.spconv_debug_set_table_slots(int(slots)))
@@ -450,4 +776,6 @@ __all__ = ["OK", "INVALID_ARG", "UNSUPPORTED", "COORD_RANGE", "DUPLICATE", "TABL
            "MAP_SORTED_KEYS", "MAP_HASH_TABLE", "MAP_SHORT_TILES", "ACTIVATIONS",
            "LIB_PATH", "EXPORTED",
            "ALGO_AUTO", "ALGO_SIMT", "ALGO_TCGEN05", "KERNEL_SIMT", "KERNEL_TCGEN05", "KERNEL_TCGEN05_GEMM",
-           "KERNEL_NAMES"]
+           "KERNEL_NAMES", "ROPE_INTERLEAVED", "ROPE_HALVES", "ROPE_LAYOUTS", "W4_MAX_ROWS", "Rope", "spconv_rms_norm",
+           "spconv_rms_norm_q8", "spconv_rms_norm_backward", "spconv_rope_create", "spconv_rope_free",
+           "spconv_rope_apply", "spconv_w4_quantize", "spconv_w4_dequantize", "spconv_linear_w4"]
