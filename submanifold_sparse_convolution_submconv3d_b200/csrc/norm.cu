@@ -14,7 +14,6 @@
 namespace spconv {
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: 1 / s stays finite
 
@@ -27,45 +26,170 @@ struct MaxNan {
     __device__ static float f(float a, float b) { return max_nan(a, b); }
 };
 
-template <typename Op>
-__device__ float block_reduce(float v) {
-    __shared__ float part[kNormThreads / 32];
-    for (int d = 16; d > 0; d >>= 1) v = Op::f(v, __shfl_xor_sync(0xffffffffu, v, d));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = Op::id();
-    for (int w = 0; w < kNormThreads / 32; ++w) v = Op::f(v, part[w]);
+// The threads of a CTA in groups of TPR, a group a row at a time: 8 or 32 lanes of a
+// warp, or the whole CTA.
+template <int TPR>
+struct Group {
+    static constexpr int kThreads = TPR > 128 ? TPR : 128;
+    static constexpr int kRows = kThreads / TPR;  // rows a CTA has in work
+};
+
+// Joins v over a row's threads; `part` (a warp's share each) is not reused within a row.
+template <typename Op, int TPR>
+__device__ __forceinline__ float row_reduce(float v, float* part) {
+#pragma unroll
+    for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) v = Op::f(v, __shfl_xor_sync(0xffffffffu, v, d));
+    if (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        if (TPR <= 256) {
+            v = part[0];
+#pragma unroll
+            for (int w = 1; w < TPR / 32; ++w) v = Op::f(v, part[w]);
+        } else {
+            const int lane = threadIdx.x & 31;
+            v = lane < TPR / 32 ? part[lane] : Op::id();
+#pragma unroll
+            for (int d = TPR / 64; d > 0; d >>= 1) v = Op::f(v, __shfl_xor_sync(0xffffffffu, v, d));
+            v = __shfl_sync(0xffffffffu, v, 0);
+        }
+    }
     return v;
 }
 
-// One CTA a row.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads)
-    k_rms_norm(const T* __restrict__ x, const T* res, const T* __restrict__ weight, int c, float eps, T* sum_out,
+// VE elements at a time: one 16-byte access, or single elements where rows do not
+// start on 16-byte boundaries.
+template <typename T, int VE>
+struct alignas(sizeof(T) * VE) Vec {
+    T v[VE];
+};
+template <typename T, int VE>
+__device__ __forceinline__ Vec<T, VE> load(const T* p) {
+    return *reinterpret_cast<const Vec<T, VE>*>(p);
+}
+
+// A row lives in its threads' registers: E elements each, in items of VE, item k of
+// thread t at (k * TPR + t) * VE.  One read of x and the residual, one write of each
+// result.
+template <typename T, int VE, int TPR, int E, bool Q8>
+__global__ void __launch_bounds__(Group<TPR>::kThreads)
+    k_rms_norm(const T* x, const T* res, const T* __restrict__ weight, int64_t n, int c, float eps, T* sum_out,
                T* __restrict__ out, float* __restrict__ rstd_out, uint8_t* __restrict__ q, float* __restrict__ scale) {
-    const int64_t base = (int64_t)blockIdx.x * c;
-    const T* r = res ? res + base : nullptr;
+    constexpr int kItems = E / VE;
+    __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
+    const int t = threadIdx.x % TPR;
+    const int64_t i = (int64_t)blockIdx.x * Group<TPR>::kRows + threadIdx.x / TPR;
+    const bool live = i < n;  // a warp's rows join their sums together, so none leaves early
+    const int64_t base = i * c;
+    float h[E];
+    Vec<T, VE> vx[kItems], vr[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int j = (k * TPR + t) * VE;
+        if (live && j < c) {
+            vx[k] = load<T, VE>(x + base + j);
+            if (res) vr[k] = load<T, VE>(res + base + j);
+        }
+    }
     float ss = 0.0f;
-    for (int j = threadIdx.x; j < c; j += kNormThreads) {
-        const float h = to_f32(x[base + j]) + (r ? to_f32(r[j]) : 0.0f);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int j = (k * TPR + t) * VE;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) h[k * VE + e] = 0.0f;
+        if (live && j < c) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                float v = to_f32(vx[k].v[e]);
+                if (res) v += to_f32(vr[k].v[e]);
+                h[k * VE + e] = v;
+                ss += v * v;
+            }
+            if (sum_out) {
+                Vec<T, VE> o;
+#pragma unroll
+                for (int e = 0; e < VE; ++e) o.v[e] = from_f32<T>(h[k * VE + e]);
+                *reinterpret_cast<Vec<T, VE>*>(sum_out + base + j) = o;
+            }
+        }
+    }
+    const float rstd = rsqrtf(row_reduce<Sum, TPR>(ss, part[0]) / (float)c + eps);
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int j = (k * TPR + t) * VE;
+        if (!live || j >= c) continue;
+        Vec<T, VE> w;
+        if (weight) w = load<T, VE>(weight + j);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            float& y = h[k * VE + e];
+            y = y * rstd * (weight ? to_f32(w.v[e]) : 1.0f);
+            if (Q8) m = max_nan(m, fabsf(y));
+        }
+        if (!Q8) {
+            Vec<T, VE> o;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) o.v[e] = from_f32<T>(h[k * VE + e]);
+            *reinterpret_cast<Vec<T, VE>*>(out + base + j) = o;
+        }
+    }
+    if (Q8) {
+        const float s = max_nan(row_reduce<MaxNan, TPR>(m, part[1]) / kE4m3Max, kMinScale);
+        const float inv = 1.0f / s;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int j = (k * TPR + t) * VE;
+            if (!live || j >= c) continue;
+            if (VE == 1) {
+                q[base + j] = __nv_cvt_float_to_fp8(h[k] * inv, __NV_SATFINITE, __NV_E4M3);
+            } else {
+                alignas(VE) __nv_fp8x2_storage_t o[VE / 2 > 0 ? VE / 2 : 1];
+#pragma unroll
+                for (int e = 0; e + 1 < VE; e += 2)
+                    o[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(h[k * VE + e] * inv, h[k * VE + e + 1] * inv),
+                                                        __NV_SATFINITE, __NV_E4M3);
+                if (VE == 8)
+                    *reinterpret_cast<uint2*>(q + base + j) = *reinterpret_cast<uint2*>(o);
+                else
+                    *reinterpret_cast<uint32_t*>(q + base + j) = *reinterpret_cast<uint32_t*>(o);
+            }
+        }
+        if (live && t == 0) scale[i] = s;
+    }
+    if (rstd_out && live && t == 0) rstd_out[i] = rstd;
+}
+
+// Rows longer than 32,768 channels: one CTA a row, read once more for each step.
+constexpr int kLongThreads = 1024;
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads)
+    k_rms_norm_long(const T* x, const T* res, const T* __restrict__ weight, int c, float eps, T* sum_out,
+                    T* __restrict__ out, float* __restrict__ rstd_out, uint8_t* __restrict__ q,
+                    float* __restrict__ scale) {
+    __shared__ float part[2][kLongThreads / 32];
+    const int64_t base = (int64_t)blockIdx.x * c;
+    float ss = 0.0f;
+    for (int j = threadIdx.x; j < c; j += kLongThreads) {
+        const float h = to_f32(x[base + j]) + (res ? to_f32(res[base + j]) : 0.0f);
         ss += h * h;
     }
-    const float rstd = rsqrtf(block_reduce<Sum>(ss) / (float)c + eps);
+    const float rstd = rsqrtf(row_reduce<Sum, kLongThreads>(ss, part[0]) / (float)c + eps);
     float s = 1.0f;
     if (q) {
         float m = 0.0f;
-        for (int j = threadIdx.x; j < c; j += kNormThreads) {
-            const float h = to_f32(x[base + j]) + (r ? to_f32(r[j]) : 0.0f);
+        for (int j = threadIdx.x; j < c; j += kLongThreads) {
+            const float h = to_f32(x[base + j]) + (res ? to_f32(res[base + j]) : 0.0f);
             m = max_nan(m, fabsf(h * rstd * (weight ? to_f32(weight[j]) : 1.0f)));
         }
-        s = max_nan(block_reduce<MaxNan>(m) / kE4m3Max, kMinScale);
+        s = max_nan(row_reduce<MaxNan, kLongThreads>(m, part[1]) / kE4m3Max, kMinScale);
     }
-    for (int j = threadIdx.x; j < c; j += kNormThreads) {
-        const float h = to_f32(x[base + j]) + (r ? to_f32(r[j]) : 0.0f);
+    const float inv = 1.0f / s;
+    for (int j = threadIdx.x; j < c; j += kLongThreads) {
+        const float h = to_f32(x[base + j]) + (res ? to_f32(res[base + j]) : 0.0f);
         const float y = h * rstd * (weight ? to_f32(weight[j]) : 1.0f);
         if (q)
-            q[base + j] = __nv_cvt_float_to_fp8(y / s, __NV_SATFINITE, __NV_E4M3);
+            q[base + j] = __nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3);
         else
             out[base + j] = from_f32<T>(y);
         if (sum_out) sum_out[base + j] = from_f32<T>(h);
@@ -76,45 +200,231 @@ __global__ void __launch_bounds__(kNormThreads)
     }
 }
 
-// One CTA a row: dx.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads)
-    k_rms_norm_dx(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
-                  const float* __restrict__ rstd_in, const T* dsum, int c, T* dx) {
-    const int64_t base = (int64_t)blockIdx.x * c;
-    const float rstd = rstd_in[blockIdx.x];
-    float dot = 0.0f;
-    for (int j = threadIdx.x; j < c; j += kNormThreads)
-        dot += to_f32(dy[base + j]) * (weight ? to_f32(weight[j]) : 1.0f) * to_f32(h[base + j]) * rstd;
-    const float mean = block_reduce<Sum>(dot) / (float)c;
-    for (int j = threadIdx.x; j < c; j += kNormThreads) {
-        const float g = to_f32(dy[base + j]) * (weight ? to_f32(weight[j]) : 1.0f);
-        float d = rstd * (g - to_f32(h[base + j]) * rstd * mean);
-        if (dsum) d += to_f32(dsum[base + j]);
-        dx[base + j] = from_f32<T>(d);
+// Row groups that share the rows of the gradient: a constant, so that the order of
+// the column sums depends on the shape alone.
+constexpr int kMaxParts = 592;
+inline int row_parts(int64_t n, int rows) {
+    const int64_t need = (n + rows - 1) / rows;
+    return (int)(need < kMaxParts ? need : kMaxParts);
+}
+
+// dx of the rows and, in `part`, each CTA's column sums of dy * xh.  A CTA's row groups
+// take rows blockIdx.x * kRows + group, and so on by gridDim.x * kRows; a thread keeps
+// the sums of its columns in registers over all its rows, and the groups' sums are
+// joined in shared memory at the end.
+template <typename T, int VE, int TPR, int E>
+__global__ void __launch_bounds__(Group<TPR>::kThreads)
+    k_rms_norm_backward(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
+                        const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
+                        float* __restrict__ part) {
+    constexpr int kItems = E / VE, kRows = Group<TPR>::kRows;
+    __shared__ float red[2][TPR > 32 ? TPR / 32 : 1];
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    float dw[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[e] = 0.0f;
+    int turn = 0;
+    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += (int64_t)gridDim.x * kRows, turn ^= 1) {
+        const int64_t i = i0 + group;
+        const bool live = i < n;
+        const int64_t base = i * c;
+        Vec<T, VE> vd[kItems], vh[kItems], vs[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int j = (k * TPR + t) * VE;
+            if (live && j < c) {
+                vd[k] = load<T, VE>(dy + base + j);
+                vh[k] = load<T, VE>(h + base + j);
+                if (dsum) vs[k] = load<T, VE>(dsum + base + j);
+            }
+        }
+        const float rstd = live ? rstd_in[i] : 0.0f;
+        float dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int j = (k * TPR + t) * VE;
+            if (!live || j >= c) continue;
+            Vec<T, VE> w;
+            if (weight) w = load<T, VE>(weight + j);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float dxh = to_f32(vd[k].v[e]) * (to_f32(vh[k].v[e]) * rstd);
+                dw[k * VE + e] += dxh;
+                dot += dxh * (weight ? to_f32(w.v[e]) : 1.0f);
+            }
+        }
+        const float mean = row_reduce<Sum, TPR>(dot, red[turn]) / (float)c;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int j = (k * TPR + t) * VE;
+            if (!live || j >= c) continue;
+            Vec<T, VE> w, o;
+            if (weight) w = load<T, VE>(weight + j);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const float g = to_f32(vd[k].v[e]) * (weight ? to_f32(w.v[e]) : 1.0f);
+                float d = rstd * (g - to_f32(vh[k].v[e]) * rstd * mean);
+                if (dsum) d += to_f32(vs[k].v[e]);
+                o.v[e] = from_f32<T>(d);
+            }
+            *reinterpret_cast<Vec<T, VE>*>(dx + base + j) = o;
+        }
+    }
+    if (!part) return;
+    part += (int64_t)blockIdx.x * c;
+    if (kRows == 1) {
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int j = (k * TPR + t) * VE;
+            if (j >= c) continue;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) part[j + e] = dw[k * VE + e];
+        }
+    } else {
+        constexpr int kCols = TPR * E, kWarps = Group<TPR>::kThreads / 32;
+        __shared__ float cols[kRows == 1 ? 1 : kWarps][kRows == 1 ? 1 : kCols];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            for (int d = TPR; d < 32; d <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], d);
+        if ((threadIdx.x & 31) < TPR) {
+#pragma unroll
+            for (int k = 0; k < kItems; ++k)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) cols[threadIdx.x / 32][(k * TPR + t) * VE + e] = dw[k * VE + e];
+        }
+        __syncthreads();
+        for (int j = threadIdx.x; j < c; j += Group<TPR>::kThreads) {
+            float s = cols[0][j];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) s += cols[w][j];
+            part[j] = s;
+        }
     }
 }
 
-constexpr int kMaxParts = 512;
-inline int weight_parts(int64_t n) { return (int)(n < kMaxParts ? n : kMaxParts); }
-
-// part[p][j] = sum of dy * h * rstd over the rows p, p + parts, ...
 template <typename T>
-__global__ void __launch_bounds__(kNormThreads)
-    k_rms_norm_dw_part(const T* __restrict__ dy, const T* __restrict__ h, const float* __restrict__ rstd, int64_t n,
-                       int c, float* __restrict__ part) {
-    for (int j = threadIdx.x; j < c; j += kNormThreads) {
-        float s = 0.0f;
-        for (int64_t i = blockIdx.x; i < n; i += gridDim.x) s += to_f32(dy[i * c + j]) * to_f32(h[i * c + j]) * rstd[i];
-        part[(int64_t)blockIdx.x * c + j] = s;
+__global__ void __launch_bounds__(kLongThreads)
+    k_rms_norm_backward_long(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
+                             const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
+                             float* __restrict__ part) {
+    __shared__ float red[2][kLongThreads / 32];
+    int turn = 0;
+    for (int64_t i = blockIdx.x; i < n; i += gridDim.x, turn ^= 1) {
+        const int64_t base = i * c;
+        const float rstd = rstd_in[i];
+        float dot = 0.0f;
+        for (int j = threadIdx.x; j < c; j += kLongThreads) {
+            const float dxh = to_f32(dy[base + j]) * (to_f32(h[base + j]) * rstd);
+            if (part) {
+                float* p = part + (int64_t)blockIdx.x * c + j;
+                *p = i == blockIdx.x ? dxh : *p + dxh;
+            }
+            dot += dxh * (weight ? to_f32(weight[j]) : 1.0f);
+        }
+        const float mean = row_reduce<Sum, kLongThreads>(dot, red[turn]) / (float)c;
+        for (int j = threadIdx.x; j < c; j += kLongThreads) {
+            const float g = to_f32(dy[base + j]) * (weight ? to_f32(weight[j]) : 1.0f);
+            float d = rstd * (g - to_f32(h[base + j]) * rstd * mean);
+            if (dsum) d += to_f32(dsum[base + j]);
+            dx[base + j] = from_f32<T>(d);
+        }
     }
 }
-__global__ void k_rms_norm_dw(const float* __restrict__ part, int parts, int c, float* __restrict__ dweight) {
-    const int j = blockIdx.x * blockDim.x + threadIdx.x;
-    if (j >= c) return;
+
+// dweight[j] = sum over the parts, in a fixed order: a CTA takes 32 columns, its 8
+// warps every 8th part, joined in warp order.
+__global__ void __launch_bounds__(256) k_rms_norm_dw(const float* __restrict__ part, int parts, int c,
+                                                     float* __restrict__ dweight) {
+    __shared__ float sum[8][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int p = 0; p < parts; ++p) s += part[(int64_t)p * c + j];
-    dweight[j] = s;
+    if (j < c) {
+#pragma unroll 8
+        for (int p = warp; p < parts; p += 8) s += part[(int64_t)p * c + j];
+    }
+    sum[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && j < c) {
+        for (int w = 1; w < 8; ++w) s += sum[w][lane];
+        dweight[j] = s;
+    }
+}
+
+struct NormArgs {
+    const void *x, *res, *weight;
+    int64_t n;
+    int c;
+    float eps;
+    void *sum_out, *out;
+    float* rstd;
+    uint8_t* q;
+    float* scale;
+    // gradient
+    const void* dsum;
+    const float* rstd_in;
+    void* dx;
+    float* part;
+    cudaStream_t stream;
+};
+
+enum class NormPass { kRows, kQ8, kBackward };
+
+template <typename T, int VE, int TPR, int E, NormPass P>
+void launch_norm_as(const NormArgs& a, int* parts) {
+    constexpr int kRows = Group<TPR>::kRows, kThreads = Group<TPR>::kThreads;
+    if (P == NormPass::kBackward) {
+        *parts = row_parts(a.n, kRows);
+        k_rms_norm_backward<T, VE, TPR, E><<<*parts, kThreads, 0, a.stream>>>(
+            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
+            static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
+    } else {
+        k_rms_norm<T, VE, TPR, E, P == NormPass::kQ8><<<(unsigned)((a.n + kRows - 1) / kRows), kThreads, 0, a.stream>>>(
+            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.n, a.c, a.eps,
+            static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
+    }
+}
+
+// A thread holds up to 32 elements of a row; the fewest threads that hold it take it.
+template <typename T, NormPass P>
+void launch_norm(const NormArgs& a, int* parts) {
+    constexpr int kVe = 16 / (int)sizeof(T);
+    if (a.c > 32768) {
+        if (P == NormPass::kBackward) {
+            *parts = row_parts(a.n, 1);
+            k_rms_norm_backward_long<T><<<*parts, kLongThreads, 0, a.stream>>>(
+                static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
+                static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
+        } else {
+            k_rms_norm_long<T><<<(unsigned)a.n, kLongThreads, 0, a.stream>>>(
+                static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.c, a.eps,
+                static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
+        }
+    } else if (a.c % kVe == 0) {
+        if (a.c <= 64) launch_norm_as<T, kVe, 8, 8, P>(a, parts);
+        else if (a.c <= 128) launch_norm_as<T, kVe, 8, 16, P>(a, parts);
+        else if (a.c <= 256) launch_norm_as<T, kVe, 8, 32, P>(a, parts);
+        else if (a.c <= 512) launch_norm_as<T, kVe, 32, 16, P>(a, parts);
+        else if (a.c <= 1024) launch_norm_as<T, kVe, 32, 32, P>(a, parts);
+        else if (a.c <= 2048) launch_norm_as<T, kVe, 128, 16, P>(a, parts);
+        else if (a.c <= 4096) launch_norm_as<T, kVe, 128, 32, P>(a, parts);
+        else if (a.c <= 8192) launch_norm_as<T, kVe, 256, 32, P>(a, parts);
+        else if (a.c <= 16384) launch_norm_as<T, kVe, 512, 32, P>(a, parts);
+        else launch_norm_as<T, kVe, 1024, 32, P>(a, parts);
+    } else {
+        if (a.c <= 256) launch_norm_as<T, 1, 32, 8, P>(a, parts);
+        else if (a.c <= 512) launch_norm_as<T, 1, 32, 16, P>(a, parts);
+        else if (a.c <= 1024) launch_norm_as<T, 1, 32, 32, P>(a, parts);
+        else if (a.c <= 4096) launch_norm_as<T, 1, 128, 32, P>(a, parts);
+        else launch_norm_as<T, 1, 1024, 32, P>(a, parts);
+    }
+}
+
+template <NormPass P>
+void launch_norm_type(spconv_dtype_t dtype, const NormArgs& a, int* parts) {
+    if (dtype == SPCONV_BF16)
+        launch_norm<__nv_bfloat16, P>(a, parts);
+    else
+        launch_norm<float, P>(a, parts);
 }
 
 spconv_status_t norm_args(spconv_dtype_t dtype, const void* x, const void* residual, const void* weight, int64_t n,
@@ -142,27 +452,6 @@ bool hits_inputs(const void* p, int64_t pbytes, const void* x, const void* resid
            overlaps(p, pbytes, weight, wbytes) || overlaps(p, pbytes, sum_out, bytes);
 }
 
-template <typename T>
-void launch_norm(const void* x, const void* residual, const void* weight, int64_t n, int c, float eps, void* sum_out,
-                 void* out, float* rstd, uint8_t* q, float* scale, cudaStream_t st) {
-    k_rms_norm<T><<<(unsigned)n, kNormThreads, 0, st>>>(
-        static_cast<const T*>(x), static_cast<const T*>(residual), static_cast<const T*>(weight), c, eps,
-        static_cast<T*>(sum_out), static_cast<T*>(out), rstd, q, scale);
-}
-
-template <typename T>
-void launch_norm_backward(const void* dy, const void* h, const void* weight, const float* rstd, const void* dsum,
-                          int64_t n, int c, void* dx, float* dweight, float* ws, cudaStream_t st) {
-    k_rms_norm_dx<T><<<(unsigned)n, kNormThreads, 0, st>>>(static_cast<const T*>(dy), static_cast<const T*>(h),
-                                                           static_cast<const T*>(weight), rstd,
-                                                           static_cast<const T*>(dsum), c, static_cast<T*>(dx));
-    if (!dweight) return;
-    const int parts = weight_parts(n);
-    k_rms_norm_dw_part<T><<<parts, kNormThreads, 0, st>>>(static_cast<const T*>(dy), static_cast<const T*>(h), rstd, n,
-                                                          c, ws);
-    k_rms_norm_dw<<<(c + 255) / 256, 256, 0, st>>>(ws, parts, c, dweight);
-}
-
 }  // namespace
 }  // namespace spconv
 
@@ -181,11 +470,9 @@ spconv_status_t spconv_rms_norm(spconv_dtype_t dtype, const void* x, const void*
     if (hits_inputs(out, bytes, x, residual, weight, sum_out, bytes, wbytes) ||
         hits_inputs(rstd, n * 4, x, residual, weight, sum_out, bytes, wbytes) || overlaps(out, bytes, rstd, n * 4))
         return row_fail(SPCONV_ERR_INVALID_ARG, "out and rstd must not overlap another buffer of the call");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == SPCONV_BF16)
-        launch_norm<__nv_bfloat16>(x, residual, weight, n, channels, eps, sum_out, out, rstd, nullptr, nullptr, st);
-    else
-        launch_norm<float>(x, residual, weight, n, channels, eps, sum_out, out, rstd, nullptr, nullptr, st);
+    NormArgs a = {x, residual, weight, n, channels, eps, sum_out, out, rstd};
+    a.stream = static_cast<cudaStream_t>(stream);
+    launch_norm_type<NormPass::kRows>(dtype, a, nullptr);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm");
 }
@@ -202,11 +489,9 @@ spconv_status_t spconv_rms_norm_q8(spconv_dtype_t dtype, const void* x, const vo
         hits_inputs(scale, n * 4, x, residual, weight, sum_out, bytes, wbytes) ||
         overlaps(q, n * channels, scale, n * 4))
         return row_fail(SPCONV_ERR_INVALID_ARG, "q and scale must not overlap another buffer of the call");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == SPCONV_BF16)
-        launch_norm<__nv_bfloat16>(x, residual, weight, n, channels, eps, sum_out, nullptr, nullptr, q, scale, st);
-    else
-        launch_norm<float>(x, residual, weight, n, channels, eps, sum_out, nullptr, nullptr, q, scale, st);
+    NormArgs a = {x, residual, weight, n, channels, eps, sum_out, nullptr, nullptr, q, scale};
+    a.stream = static_cast<cudaStream_t>(stream);
+    launch_norm_type<NormPass::kQ8>(dtype, a, nullptr);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm_q8");
 }
@@ -216,7 +501,7 @@ spconv_status_t spconv_rms_norm_workspace(int64_t n, int32_t channels, int64_t* 
     if (n < 0 || n >= (int64_t(1) << 31)) return row_fail(SPCONV_ERR_INVALID_ARG, "n must be in [0, 2^31)");
     if (channels < 1 || channels > SPCONV_NORM_MAX_CHANNELS)
         return row_fail(SPCONV_ERR_INVALID_ARG, "channels must be in [1, 65536]");
-    *bytes = (int64_t)weight_parts(n) * channels * 4;
+    *bytes = (int64_t)row_parts(n, 1) * channels * 4;
     return SPCONV_OK;
 }
 
@@ -238,7 +523,7 @@ spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, c
     if (dweight && (!workspace || !is_aligned(workspace, 16)))
         return row_fail(SPCONV_ERR_INVALID_ARG, "dweight needs a 16-byte aligned workspace");
     const int64_t wbytes = (int64_t)channels * dtype_bytes(dtype), bytes = n * wbytes;
-    const int64_t wsbytes = (int64_t)weight_parts(n) * channels * 4, dwbytes = (int64_t)channels * 4;
+    const int64_t wsbytes = (int64_t)row_parts(n, 1) * channels * 4, dwbytes = (int64_t)channels * 4;
     const void* ws = dweight ? workspace : nullptr;
     bool bad = dx != dsum && overlaps(dx, bytes, dsum, bytes);
     bad = bad || overlaps(dx, bytes, dy, bytes) || overlaps(dx, bytes, h, bytes) || overlaps(dx, bytes, weight, wbytes) ||
@@ -251,12 +536,20 @@ spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, c
     if (bad)
         return row_fail(SPCONV_ERR_INVALID_ARG,
                         "dx may be dsum itself; dx, dweight and workspace must not overlap another buffer of the call");
-    if (dtype == SPCONV_BF16)
-        launch_norm_backward<__nv_bfloat16>(dy, h, weight, rstd, dsum, n, channels, dx, dweight,
-                                            static_cast<float*>(workspace), st);
-    else
-        launch_norm_backward<float>(dy, h, weight, rstd, dsum, n, channels, dx, dweight, static_cast<float*>(workspace),
-                                    st);
+    NormArgs a = {};
+    a.x = dy;
+    a.res = h;
+    a.weight = weight;
+    a.n = n;
+    a.c = channels;
+    a.dsum = dsum;
+    a.rstd_in = rstd;
+    a.dx = dx;
+    a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+    a.stream = st;
+    int parts = 0;
+    launch_norm_type<NormPass::kBackward>(dtype, a, &parts);
+    if (dweight) k_rms_norm_dw<<<(channels + 31) / 32, 256, 0, st>>>(a.part, parts, channels, dweight);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm_backward");
 }
