@@ -5,42 +5,233 @@
 //   out[i, o] = bias[o] + x_scale[i] * sum_k w[k, o] x[i, k]
 //
 // The sums are kept in fp32 and rounded once.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "row_ops.cuh"
 
 namespace spconv {
 namespace {
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t v) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+// D += A B on a 16 x 8 tile, K = 16, fp32 accumulation.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float w4_x(const float* x, int64_t i) { return x[i]; }
-__device__ __forceinline__ float w4_x(const __nv_bfloat16* x, int64_t i) { return __bfloat162float(x[i]); }
-__device__ __forceinline__ float w4_x(const uint8_t* x, int64_t i) { return e4m3_to_f32(x[i]); }
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
-// One warp an output element; a lane takes every 32nd word of 8 weights.
-template <typename T, typename X>
-__global__ void __launch_bounds__(256)
-    k_linear_w4(const X* __restrict__ x, const float* __restrict__ x_scale, int cin, const uint32_t* __restrict__ packed,
-                const T* __restrict__ scales, const T* __restrict__ offsets, int group, const T* __restrict__ bias,
-                T* __restrict__ out, int cout) {
-    const int o = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int64_t i = blockIdx.y;
-    if (o >= cout) return;
-    const int words = cin / 8, groups = cin / group;
-    float s = 0.0f;
-    for (int w = lane; w < words; w += 32) {
-        const uint32_t v = packed[(int64_t)o * words + w];
-        const int64_t g = (int64_t)o * groups + w * 8 / group;
-        const float sc = to_f32(scales[g]), of = to_f32(offsets[g]);
-        for (int e = 0; e < 8; ++e) s += (sc * (float)((v >> (4 * e)) & 15u) + of) * w4_x(x, i * cin + 8 * w + e);
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ uint32_t bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+
+// The codes i and i + 4 of a word, less 8, as two 16-bit floats.  A code placed in the
+// low mantissa bits of 128 (bf16) or 1024 (fp16) makes 128 + q or 1024 + q; taking 136 or
+// 1032 off is exact, and the sums then run on numbers of -8 .. 7.
+__device__ __forceinline__ uint32_t codes(uint32_t w, int i, __nv_bfloat16) {
+    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    return bits(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.0f)));
+}
+__device__ __forceinline__ uint32_t codes(uint32_t w, int i, __half) {
+    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+    return bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1032.0f)));
+}
+
+// Eight neighbouring elements of a row of x as the pairs (x0, x4), (x1, x5), (x2, x6),
+// (x3, x7) that meet the codes of a word, in PARTS 16-bit floats each whose sum is x.
+template <typename X>
+struct XWord;
+template <>
+struct XWord<__nv_bfloat16> {
+    using Half = __nv_bfloat16;
+    static constexpr int kParts = 1;
+    uint4 v;
+    __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ uint32_t pair(int i, int) const {
+        return __byte_perm(i < 2 ? v.x : v.y, i < 2 ? v.z : v.w, i & 1 ? 0x7632 : 0x5410);
     }
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) {
-        if (x_scale) s *= x_scale[i];
-        if (bias) s += to_f32(bias[o]);
-        out[i * cout + o] = from_f32<T>(s);
+};
+template <>
+struct XWord<__nv_fp8_e4m3> {
+    using Half = __half;  // holds every e4m3 value
+    static constexpr int kParts = 1;
+    uint2 v;
+    __device__ void load(const __nv_fp8_e4m3* p) { v = *reinterpret_cast<const uint2*>(p); }
+    __device__ void zero() { v = make_uint2(0, 0); }
+    __device__ uint32_t pair(int i, int) const {
+        const uint32_t two = __byte_perm(v.x, v.y, i | ((i + 4) << 4));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+        return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    }
+};
+template <>
+struct XWord<float> {
+    // Three bf16 parts, each the leading 8 bits (cut, so the next is exact): 24 bits in all.
+    using Half = __nv_bfloat16;
+    static constexpr int kParts = 3;
+    float v[8];
+    __device__ void load(const float* p) {
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+        *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    }
+    __device__ static uint32_t part_of(float x, int part) {
+        if (!(fabsf(x) <= 3.402823466e38f)) return part == 0 ? (x != x ? 0x7fc0u : __float_as_uint(x) >> 16) : 0u;
+        for (int k = 0; k < part; ++k) x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+        return __float_as_uint(x) >> 16;
+    }
+    __device__ uint32_t pair(int i, int part) const { return part_of(v[i], part) | (part_of(v[i + 4], part) << 16); }
+};
+
+template <typename Half>
+struct Ones {
+    static constexpr uint32_t v = std::is_same<Half, __half>::value ? 0x3c003c00u : 0x3f803f80u;
+};
+
+constexpr int kW4Warps = 8;
+constexpr int kW4Chunk = 128;  // input channels a warp takes at a time: 16 codes words a row
+
+// A warp multiplies 16 MT outputs by 8 NT rows over every kW4Warps-th chunk; the warps'
+// sums are joined in shared memory.
+//
+// Fragments.  In one 16 x 8 x 16 step lane (g, t) = (lane / 4, lane % 4) holds four
+// input channels of outputs g and g + 8 and of row g; which four is free as long as both
+// operands agree.  A group's scale must be common to the step, so lane t owns the
+// group's words [t W, t W + W), W = GROUP / 32, neighbouring in memory: W words of
+// either output with one load, and each word gives two steps.
+//
+// Scales.  Over a group, with q' = q - 8:  sum w x = s sum q' x + (z + 8 s) sum x; the
+// first sum is the step's accumulator, started at zero for each group, the second comes
+// out of the same instruction with ones in place of the codes.
+template <typename T, typename X, int MT, int NT, int GROUP>
+__global__ void __launch_bounds__(32 * kW4Warps)
+    k_linear_w4(const X* __restrict__ x, const float* __restrict__ x_scale, int n, int cin,
+                const uint32_t* __restrict__ packed, const T* __restrict__ scales, const T* __restrict__ offsets,
+                const T* __restrict__ bias, T* __restrict__ out, int cout) {
+    using Half = typename XWord<X>::Half;
+    constexpr int kParts = XWord<X>::kParts;
+    constexpr int kW = GROUP / 32, kGroups = kW4Chunk / GROUP;
+    __shared__ float join[kW4Warps][MT * 16][NT * 8 + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int o0 = blockIdx.x * MT * 16, row0 = blockIdx.y * NT * 8;
+    const int words = cin / 8, groups = cin / GROUP;
+    float y[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[m][b][e] = 0.0f;
+    for (int k0 = warp * kGroups; k0 < groups; k0 += kW4Warps * kGroups) {
+        // the chunk's codes, scales and offsets
+        uint32_t w[MT][2][kGroups][kW];
+        float s[MT][2][kGroups], z[MT][2][kGroups];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int o = o0 + m * 16 + r * 8 + g;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const bool in = o < cout && k0 + j < groups;
+                    const uint32_t* p = packed + (int64_t)o * words + (k0 + j) * (GROUP / 8) + t * kW;
+                    if (kW == 4) {
+                        const uint4 v = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+                        w[m][r][j][0] = v.x, w[m][r][j][kW > 1 ? 1 : 0] = v.y;
+                        w[m][r][j][kW > 2 ? 2 : 0] = v.z, w[m][r][j][kW > 2 ? 3 : 0] = v.w;
+                    } else if (kW == 2) {
+                        const uint2 v = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
+                        w[m][r][j][0] = v.x, w[m][r][j][kW > 1 ? 1 : 0] = v.y;
+                    } else {
+                        w[m][r][j][0] = in ? *p : 0;
+                    }
+                    const int64_t at = (int64_t)o * groups + k0 + j;
+                    s[m][r][j] = in ? to_f32(scales[at]) : 0.0f;
+                    z[m][r][j] = in ? to_f32(offsets[at]) : 0.0f;
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            float d[MT][NT][4], sum[NT][4];
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[b][e] = 0.0f;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) d[m][b][e] = 0.0f;
+                }
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+                XWord<X> xw[NT];
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    const int row = row0 + b * 8 + g;
+                    xw[b].zero();
+                    if (row < n && k0 + j < groups)
+                        xw[b].load(x + (int64_t)row * cin + (k0 + j) * GROUP + (t * kW + i) * 8);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t a[MT][4];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        a[m][0] = codes(w[m][0][j][i], 2 * half, Half());
+                        a[m][1] = codes(w[m][1][j][i], 2 * half, Half());
+                        a[m][2] = codes(w[m][0][j][i], 2 * half + 1, Half());
+                        a[m][3] = codes(w[m][1][j][i], 2 * half + 1, Half());
+                    }
+                    const uint32_t ones[4] = {Ones<Half>::v, Ones<Half>::v, Ones<Half>::v, Ones<Half>::v};
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int b = 0; b < NT; ++b) {
+                            const uint32_t b0 = xw[b].pair(2 * half, p), b1 = xw[b].pair(2 * half + 1, p);
+                            mma_16816(sum[b], ones, b0, b1, Half());
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) mma_16816(d[m][b], a[m], b0, b1, Half());
+                        }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float sc = s[m][e >> 1][j], of = fmaf(8.0f, sc, z[m][e >> 1][j]);
+                        y[m][b][e] = fmaf(sc, d[m][b][e], fmaf(of, sum[b][e & 1], y[m][b][e]));
+                    }
+        }
+    }
+    // accumulator e of lane (g, t): output g + 8 (e / 2), row 2 t + e % 2
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) join[warp][m * 16 + (e >> 1) * 8 + g][b * 8 + 2 * t + (e & 1)] = y[m][b][e];
+    __syncthreads();
+    for (int at = threadIdx.x; at < MT * 16 * NT * 8; at += 32 * kW4Warps) {
+        const int o = at % (MT * 16), r = at / (MT * 16);
+        if (o0 + o >= cout || row0 + r >= n) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kW4Warps; ++k) v += join[k][o][r];
+        if (x_scale) v *= x_scale[row0 + r];
+        if (bias) v += to_f32(bias[o0 + o]);
+        out[(int64_t)(row0 + r) * cout + o0 + o] = from_f32<T>(v);
     }
 }
 
@@ -111,12 +302,36 @@ spconv_status_t w4_args(spconv_dtype_t dtype, const void* packed, const void* sc
     return SPCONV_OK;
 }
 
+template <typename T, typename X, int MT, int NT, int GROUP>
+void launch_w4_as(const void* x, const float* x_scale, int n, int cin, const void* packed, const void* scales,
+                  const void* offsets, const void* bias, void* out, int cout, cudaStream_t st) {
+    const dim3 grid((cout + 16 * MT - 1) / (16 * MT), (n + 8 * NT - 1) / (8 * NT));
+    k_linear_w4<T, X, MT, NT, GROUP><<<grid, 32 * kW4Warps, 0, st>>>(
+        static_cast<const X*>(x), x_scale, n, cin, static_cast<const uint32_t*>(packed), static_cast<const T*>(scales),
+        static_cast<const T*>(offsets), static_cast<const T*>(bias), static_cast<T*>(out), cout);
+}
+
+template <typename T, typename X, int GROUP>
+void launch_w4_group(const void* x, const float* x_scale, int n, int cin, const void* packed, const void* scales,
+                     const void* offsets, const void* bias, void* out, int cout, cudaStream_t st) {
+    if (n <= 8) {
+        launch_w4_as<T, X, 1, 1, GROUP>(x, x_scale, n, cin, packed, scales, offsets, bias, out, cout, st);
+    } else if (n <= 16 || sizeof(X) == 4) {  // fp32 rows take three times the registers
+        launch_w4_as<T, X, 1, 2, GROUP>(x, x_scale, n, cin, packed, scales, offsets, bias, out, cout, st);
+    } else if constexpr (sizeof(X) < 4) {
+        launch_w4_as<T, X, 2, 4, GROUP>(x, x_scale, n, cin, packed, scales, offsets, bias, out, cout, st);
+    }
+}
+
 template <typename T, typename X>
 void launch_linear_w4(const void* x, const float* x_scale, int64_t n, int cin, const void* packed, const void* scales,
                       const void* offsets, int group, const void* bias, void* out, int cout, cudaStream_t st) {
-    k_linear_w4<T, X><<<dim3((cout + 7) / 8, (unsigned)n), 256, 0, st>>>(
-        static_cast<const X*>(x), x_scale, cin, static_cast<const uint32_t*>(packed), static_cast<const T*>(scales),
-        static_cast<const T*>(offsets), group, static_cast<const T*>(bias), static_cast<T*>(out), cout);
+    if (group == 32)
+        launch_w4_group<T, X, 32>(x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, st);
+    else if (group == 64)
+        launch_w4_group<T, X, 64>(x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, st);
+    else
+        launch_w4_group<T, X, 128>(x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, st);
 }
 
 }  // namespace
@@ -193,12 +408,12 @@ spconv_status_t spconv_linear_w4(spconv_dtype_t dtype, const void* x, const floa
         return row_fail(SPCONV_ERR_INVALID_ARG, "out must not overlap another buffer of the call");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == SPCONV_BF16 && x_scale)
-        launch_linear_w4<__nv_bfloat16, uint8_t>(x, x_scale, n, cin, packed, scales, offsets, group, bias, out, cout, st);
+        launch_linear_w4<__nv_bfloat16, __nv_fp8_e4m3>(x, x_scale, n, cin, packed, scales, offsets, group, bias, out, cout, st);
     else if (dtype == SPCONV_BF16)
         launch_linear_w4<__nv_bfloat16, __nv_bfloat16>(x, nullptr, n, cin, packed, scales, offsets, group, bias, out,
                                                        cout, st);
     else if (x_scale)
-        launch_linear_w4<float, uint8_t>(x, x_scale, n, cin, packed, scales, offsets, group, bias, out, cout, st);
+        launch_linear_w4<float, __nv_fp8_e4m3>(x, x_scale, n, cin, packed, scales, offsets, group, bias, out, cout, st);
     else
         launch_linear_w4<float, float>(x, nullptr, n, cin, packed, scales, offsets, group, bias, out, cout, st);
     const cudaError_t e = cudaGetLastError();
