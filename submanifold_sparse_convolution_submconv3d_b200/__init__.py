@@ -454,7 +454,13 @@ def spconv_subdivide(coords: torch.Tensor, extent, x: torch.Tensor | None = None
 
 # ------------------------------------------------------------ operators on feature rows
 # One token's row is a few microseconds of GPU work, so these calls keep the host side
-# short: they enter a device or stream context only where it is not current already.
+# short: they enter a device or stream context only where it is not current already, ask
+# torch for the current stream's handle without making a Stream object (0.1 us against
+# 3.2) and make results like an input where they can (1.3 us against 2.4).
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _elsewhere(x: torch.Tensor, stream) -> bool:
     return stream is not None or x.device.index != torch.cuda.current_device()
@@ -492,13 +498,19 @@ def _like(t, shape, dtype, device, what: str) -> None:
                          f"{str(t.dtype)[6:]} {list(t.shape)} on {t.device}")
 
 
-def _out(t, shape, dtype, device, what: str) -> torch.Tensor:
+def _out(t, like: torch.Tensor, shape, dtype, what: str) -> torch.Tensor:
+    """The result tensor the caller gave, checked, or a new one on ``like``'s device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _like(t, shape, dtype, device, what)
+        return like.new_empty(shape, dtype=dtype)
+    _like(t, shape, dtype, like.device, what)
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t
+
+
+def _out_like(t, like: torch.Tensor, what: str) -> torch.Tensor:
+    """``_out`` of the shape and type of ``like``, which is contiguous."""
+    return torch.empty_like(like) if t is None else _out(t, like, like.shape, like.dtype, what)
 
 
 def _norm_rows(x, weight, what: str) -> None:
@@ -506,6 +518,17 @@ def _norm_rows(x, weight, what: str) -> None:
         raise ValueError(f"{what} must be a float32 or bfloat16 CUDA tensor [N, C]")
     if weight is not None:
         _like(weight, (x.shape[1],), x.dtype, x.device, "weight")
+
+
+def _norm_inputs(x, weight, residual, sum_out) -> tuple:
+    if residual is not None:
+        _like(residual, x.shape, x.dtype, x.device, "residual")
+        residual = _in(residual)
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    x = _in(x)
+    return (x, None if weight is None else _in(weight), residual,
+            None if residual is None else _out_like(sum_out, x, "sum_out"))
 
 
 def spconv_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
@@ -520,19 +543,13 @@ def spconv_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residua
     if _elsewhere(x, stream):
         with _on(x.device, stream):
             return spconv_rms_norm(x, weight, residual, eps, out, sum_out, rstd)
-    if residual is not None:
-        _like(residual, x.shape, x.dtype, x.device, "residual")
-        sum_out = _out(sum_out, x.shape, x.dtype, x.device, "sum_out")
-        residual = _in(residual)
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
+    n, c = x.shape
+    x, weight, residual, sum_out = _norm_inputs(x, weight, residual, sum_out)
     if rstd is not None:
-        _out(rstd, (x.shape[0],), torch.float32, x.device, "rstd")
-    out = _out(out, x.shape, x.dtype, x.device, "out")
-    x = _in(x)
-    weight = None if weight is None else _in(weight)
-    _check(lib.spconv_rms_norm(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), x.shape[0], x.shape[1],
-                               eps, _ptr(sum_out), out.data_ptr(), _ptr(rstd), _stream(None)))
+        _out(rstd, x, (n,), torch.float32, "rstd")
+    out = _out_like(out, x, "out")
+    _check(lib.spconv_rms_norm(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), n, c, eps,
+                               _ptr(sum_out), out.data_ptr(), _ptr(rstd), _raw_stream(x.get_device())))
     return out if residual is None else (out, sum_out)
 
 
@@ -547,18 +564,12 @@ def spconv_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, resi
     if _elsewhere(x, stream):
         with _on(x.device, stream):
             return spconv_rms_norm_q8(x, weight, residual, eps, out, scale, sum_out)
-    if residual is not None:
-        _like(residual, x.shape, x.dtype, x.device, "residual")
-        sum_out = _out(sum_out, x.shape, x.dtype, x.device, "sum_out")
-        residual = _in(residual)
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    out = _out(out, x.shape, torch.float8_e4m3fn, x.device, "out")
-    scale = _out(scale, (x.shape[0],), torch.float32, x.device, "scale")
-    x = _in(x)
-    weight = None if weight is None else _in(weight)
-    _check(lib.spconv_rms_norm_q8(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), x.shape[0], x.shape[1],
-                                  eps, _ptr(sum_out), out.data_ptr(), scale.data_ptr(), _stream(None)))
+    n, c = x.shape
+    x, weight, residual, sum_out = _norm_inputs(x, weight, residual, sum_out)
+    out = _out(out, x, (n, c), torch.float8_e4m3fn, "out")
+    scale = _out(scale, x, (n,), torch.float32, "scale")
+    _check(lib.spconv_rms_norm_q8(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), n, c, eps,
+                                  _ptr(sum_out), out.data_ptr(), scale.data_ptr(), _raw_stream(x.get_device())))
     return (out, scale) if residual is None else (out, scale, sum_out)
 
 
@@ -580,19 +591,19 @@ def spconv_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
     if dsum is not None:
         _like(dsum, h.shape, h.dtype, h.device, "dsum")
         dsum = _in(dsum)
-    dx = _out(dx, h.shape, h.dtype, h.device, "dx")
+    dy, h, rstd = _in(dy), _in(h), _in(rstd)
+    dx = _out_like(dx, h, "dx")
     dweight = workspace = None
     if weight is not None:
         weight = _in(weight)
         if weight_grad:
             size = ctypes.c_int64()
             _check(lib.spconv_rms_norm_workspace(n, c, ctypes.byref(size)))
-            workspace = torch.empty(max(size.value, 16), dtype=torch.uint8, device=h.device)
-            dweight = torch.empty(c, dtype=torch.float32, device=h.device)
-    dy, h, rstd = _in(dy), _in(h), _in(rstd)
+            workspace = rstd.new_empty(size.value // 4)
+            dweight = rstd.new_empty(c)
     _check(lib.spconv_rms_norm_backward(_DTYPES[h.dtype], dy.data_ptr(), h.data_ptr(), _ptr(weight), rstd.data_ptr(),
                                         _ptr(dsum), n, c, dx.data_ptr(), _ptr(dweight), _ptr(workspace),
-                                        _stream(None)))
+                                        _raw_stream(h.get_device())))
     return dx, dweight
 
 
@@ -661,7 +672,7 @@ def spconv_rope_apply(rope: Rope, coords: torch.Tensor, x: torch.Tensor, out: to
             return spconv_rope_apply(rope, coords, x, out, inverse)
     n, heads, d = x.shape
     if out is None:
-        out = torch.empty((n, heads, d), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty((n, heads, d))
     else:
         _like(out, x.shape, x.dtype, x.device, "out")
         if out.stride(2) != 1:
@@ -671,7 +682,7 @@ def spconv_rope_apply(rope: Rope, coords: torch.Tensor, x: torch.Tensor, out: to
     coords = _in(coords)
     _check(lib.spconv_rope_apply(rope.handle, _DTYPES[x.dtype], coords.data_ptr(), n, x.data_ptr(), heads, x.stride(0),
                                  x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), bool(inverse),
-                                 _stream(None)))
+                                 _raw_stream(x.get_device())))
     return out
 
 
@@ -703,10 +714,10 @@ def spconv_w4_quantize(w: torch.Tensor, group: int = 64, stream=None) -> tuple:
         with _on(w.device, stream):
             return spconv_w4_quantize(w, group)
     w = _in(w)
-    packed = torch.empty((cout, cin // 8), dtype=torch.int32, device=w.device)
-    scales, offsets = (torch.empty((cout, cin // group), dtype=w.dtype, device=w.device) for _ in range(2))
+    packed = w.new_empty((cout, cin // 8), dtype=torch.int32)
+    scales, offsets = w.new_empty((cout, cin // group)), w.new_empty((cout, cin // group))
     _check(lib.spconv_w4_quantize(_DTYPES[w.dtype], w.data_ptr(), cin, cout, group, packed.data_ptr(),
-                                  scales.data_ptr(), offsets.data_ptr(), _stream(None)))
+                                  scales.data_ptr(), offsets.data_ptr(), _raw_stream(w.get_device())))
     return packed, scales, offsets
 
 
@@ -719,10 +730,10 @@ def spconv_w4_dequantize(packed: torch.Tensor, scales: torch.Tensor, offsets: to
     if _elsewhere(scales, stream):
         with _on(scales.device, stream):
             return spconv_w4_dequantize(packed, scales, offsets, out)
-    out = _out(out, (1, cin, cout), scales.dtype, scales.device, "out")
+    out = _out(out, scales, (1, cin, cout), scales.dtype, "out")
     packed, scales, offsets = _in(packed), _in(scales), _in(offsets)
     _check(lib.spconv_w4_dequantize(_DTYPES[scales.dtype], packed.data_ptr(), scales.data_ptr(), offsets.data_ptr(),
-                                    cin, cout, group, out.data_ptr(), _stream(None)))
+                                    cin, cout, group, out.data_ptr(), _raw_stream(scales.get_device())))
     return out
 
 
@@ -745,11 +756,11 @@ def spconv_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     if bias is not None:
         _like(bias, (cout,), dtype, device, "bias")
         bias = _in(bias)
-    out = _out(out, (n, cout), dtype, device, "out")
+    out = _out(out, scales, (n, cout), dtype, "out")
     x, packed, scales, offsets = _in(x), _in(packed), _in(scales), _in(offsets)
     _check(lib.spconv_linear_w4(_DTYPES[dtype], x.data_ptr(), _ptr(x_scale), n, cin, packed.data_ptr(),
                                 scales.data_ptr(), offsets.data_ptr(), group, _ptr(bias), out.data_ptr(), cout,
-                                _stream(None)))
+                                _raw_stream(scales.get_device())))
     return out
 
 

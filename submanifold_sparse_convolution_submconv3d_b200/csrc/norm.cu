@@ -200,30 +200,57 @@ __global__ void __launch_bounds__(kLongThreads)
     }
 }
 
-// Row groups that share the rows of the gradient: a constant, so that the order of
-// the column sums depends on the shape alone.
-constexpr int kMaxParts = 592;
+// CTAs that share the rows of the gradient: a constant, so that the order of the column
+// sums depends on the shape alone.  Two CTAs of 512 threads fill an SM's registers.
+constexpr int kMaxParts = 2 * 148;
 inline int row_parts(int64_t n, int rows) {
     const int64_t need = (n + rows - 1) / rows;
     return (int)(need < kMaxParts ? need : kMaxParts);
 }
 
+// Sum over the TPR threads of a row group of a CTA that holds several.
+template <int TPR>
+__device__ __forceinline__ float group_sum(float v, float* part, int group) {
+#pragma unroll
+    for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+        const float* mine = part + group * kWarps;
+        v = 0.0f;
+        if (kWarps <= 4) {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += mine[w];
+        } else {
+            const int lane = threadIdx.x & 31;
+            v = lane < kWarps ? mine[lane] : 0.0f;
+#pragma unroll
+            for (int d = kWarps / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            v = __shfl_sync(0xffffffffu, v, 0);
+        }
+    }
+    return v;
+}
+
 // dx of the rows and, in `part`, each CTA's column sums of dy * xh.  A CTA's row groups
-// take rows blockIdx.x * kRows + group, and so on by gridDim.x * kRows; a thread keeps
-// the sums of its columns in registers over all its rows, and the groups' sums are
-// joined in shared memory at the end.
+// of TPR threads take rows blockIdx.x * kRows + group, and so on by gridDim.x * kRows,
+// and wait only within the group; a thread keeps the sums of its columns in registers
+// over all its rows, and the groups' sums are joined in shared memory at the end.
+// Few elements a thread (E = 8 up to 4096 channels) leave room for 32 warps an SM,
+// whose loads cover each other's reductions.
 template <typename T, int VE, int TPR, int E>
-__global__ void __launch_bounds__(Group<TPR>::kThreads)
+__global__ void __launch_bounds__(TPR > 512 ? TPR : 512, E == 8 ? 2 : 1)
     k_rms_norm_backward(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
                         const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
                         float* __restrict__ part) {
-    constexpr int kItems = E / VE, kRows = Group<TPR>::kRows;
-    __shared__ float red[2][TPR > 32 ? TPR / 32 : 1];
+    constexpr int kThreads = TPR > 512 ? TPR : 512, kRows = kThreads / TPR, kItems = E / VE;
+    __shared__ float red[2][kThreads / 32];
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     float dw[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = 0.0f;
-    int turn = 0;
+    int turn = 0;  // the sums' buffer: a thread may still read the last row's
     for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += (int64_t)gridDim.x * kRows, turn ^= 1) {
         const int64_t i = i0 + group;
         const bool live = i < n;
@@ -253,7 +280,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
                 dot += dxh * (weight ? to_f32(w.v[e]) : 1.0f);
             }
         }
-        const float mean = row_reduce<Sum, TPR>(dot, red[turn]) / (float)c;
+        const float mean = group_sum<TPR>(dot, red[turn], group) / (float)c;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int j = (k * TPR + t) * VE;
@@ -272,7 +299,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
     }
     if (!part) return;
     part += (int64_t)blockIdx.x * c;
-    if (kRows == 1) {
+    if constexpr (kRows == 1) {
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int j = (k * TPR + t) * VE;
@@ -281,22 +308,25 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
             for (int e = 0; e < VE; ++e) part[j + e] = dw[k * VE + e];
         }
     } else {
-        constexpr int kCols = TPR * E, kWarps = Group<TPR>::kThreads / 32;
-        __shared__ float cols[kRows == 1 ? 1 : kWarps][kRows == 1 ? 1 : kCols];
+        // a warp's groups first (TPR < 32), then the groups: kShares rows of sums
+        constexpr int kShares = TPR < 32 ? kThreads / 32 : kRows;
+        __shared__ float cols[kShares][TPR * E];
 #pragma unroll
         for (int e = 0; e < E; ++e)
+#pragma unroll
             for (int d = TPR; d < 32; d <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], d);
-        if ((threadIdx.x & 31) < TPR) {
+        if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
 #pragma unroll
             for (int k = 0; k < kItems; ++k)
 #pragma unroll
-                for (int e = 0; e < VE; ++e) cols[threadIdx.x / 32][(k * TPR + t) * VE + e] = dw[k * VE + e];
+                for (int e = 0; e < VE; ++e)
+                    cols[TPR < 32 ? threadIdx.x / 32 : group][(k * TPR + t) * VE + e] = dw[k * VE + e];
         }
         __syncthreads();
-        for (int j = threadIdx.x; j < c; j += Group<TPR>::kThreads) {
+        for (int j = threadIdx.x; j < c; j += kThreads) {
             float s = cols[0][j];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) s += cols[w][j];
+            for (int w = 1; w < kShares; ++w) s += cols[w][j];
             part[j] = s;
         }
     }
@@ -331,23 +361,39 @@ __global__ void __launch_bounds__(kLongThreads)
     }
 }
 
-// dweight[j] = sum over the parts, in a fixed order: a CTA takes 32 columns, its 8
-// warps every 8th part, joined in warp order.
-__global__ void __launch_bounds__(256) k_rms_norm_dw(const float* __restrict__ part, int parts, int c,
-                                                     float* __restrict__ dweight) {
-    __shared__ float sum[8][33];
+// dweight[j] = sum over the parts, in a fixed order: a CTA takes 32 columns, its warps
+// every 32nd part, joined by a tree.  Launched to start while the gradient's last
+// CTAs still run; it waits for them before it reads.
+__global__ void __launch_bounds__(1024) k_rms_norm_dw(const float* __restrict__ part, int parts, int c,
+                                                      float* __restrict__ dweight) {
+    __shared__ float sum[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
+    cudaGridDependencySynchronize();
     float s = 0.0f;
     if (j < c) {
-#pragma unroll 8
-        for (int p = warp; p < parts; p += 8) s += part[(int64_t)p * c + j];
+#pragma unroll 7
+        for (int p = warp; p < parts; p += 32) s += part[(int64_t)p * c + j];
     }
     sum[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && j < c) {
-        for (int w = 1; w < 8; ++w) s += sum[w][lane];
-        dweight[j] = s;
-    }
+    // column `warp`: its 32 shares to one warp
+    s = sum[lane][warp];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0 && blockIdx.x * 32 + warp < c) dweight[blockIdx.x * 32 + warp] = s;
+}
+
+cudaError_t launch_dw(const float* part, int parts, int c, float* dweight, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((c + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_rms_norm_dw, part, parts, c, dweight);
 }
 
 struct NormArgs {
@@ -367,64 +413,80 @@ struct NormArgs {
     cudaStream_t stream;
 };
 
-enum class NormPass { kRows, kQ8, kBackward };
-
-template <typename T, int VE, int TPR, int E, NormPass P>
-void launch_norm_as(const NormArgs& a, int* parts) {
+template <typename T, int VE, int TPR, int E, bool Q8>
+void launch_forward_as(const NormArgs& a) {
     constexpr int kRows = Group<TPR>::kRows, kThreads = Group<TPR>::kThreads;
-    if (P == NormPass::kBackward) {
-        *parts = row_parts(a.n, kRows);
-        k_rms_norm_backward<T, VE, TPR, E><<<*parts, kThreads, 0, a.stream>>>(
-            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
-            static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
-    } else {
-        k_rms_norm<T, VE, TPR, E, P == NormPass::kQ8><<<(unsigned)((a.n + kRows - 1) / kRows), kThreads, 0, a.stream>>>(
-            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.n, a.c, a.eps,
-            static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
-    }
+    k_rms_norm<T, VE, TPR, E, Q8><<<(unsigned)((a.n + kRows - 1) / kRows), kThreads, 0, a.stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.n, a.c, a.eps,
+        static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
+}
+
+// Returns the CTAs that wrote column sums.
+template <typename T, int VE, int TPR, int E>
+int launch_backward_as(const NormArgs& a) {
+    constexpr int kThreads = TPR > 512 ? TPR : 512;
+    const int parts = row_parts(a.n, kThreads / TPR);
+    k_rms_norm_backward<T, VE, TPR, E><<<parts, kThreads, 0, a.stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
+        static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
+    return parts;
 }
 
 // A thread holds up to 32 elements of a row; the fewest threads that hold it take it.
-template <typename T, NormPass P>
-void launch_norm(const NormArgs& a, int* parts) {
+template <typename T, bool Q8>
+void launch_forward(const NormArgs& a) {
     constexpr int kVe = 16 / (int)sizeof(T);
     if (a.c > 32768) {
-        if (P == NormPass::kBackward) {
-            *parts = row_parts(a.n, 1);
-            k_rms_norm_backward_long<T><<<*parts, kLongThreads, 0, a.stream>>>(
-                static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
-                static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
-        } else {
-            k_rms_norm_long<T><<<(unsigned)a.n, kLongThreads, 0, a.stream>>>(
-                static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.c, a.eps,
-                static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
-        }
+        k_rms_norm_long<T><<<(unsigned)a.n, kLongThreads, 0, a.stream>>>(
+            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.c, a.eps,
+            static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
     } else if (a.c % kVe == 0) {
-        if (a.c <= 64) launch_norm_as<T, kVe, 8, 8, P>(a, parts);
-        else if (a.c <= 128) launch_norm_as<T, kVe, 8, 16, P>(a, parts);
-        else if (a.c <= 256) launch_norm_as<T, kVe, 8, 32, P>(a, parts);
-        else if (a.c <= 512) launch_norm_as<T, kVe, 32, 16, P>(a, parts);
-        else if (a.c <= 1024) launch_norm_as<T, kVe, 32, 32, P>(a, parts);
-        else if (a.c <= 2048) launch_norm_as<T, kVe, 128, 16, P>(a, parts);
-        else if (a.c <= 4096) launch_norm_as<T, kVe, 128, 32, P>(a, parts);
-        else if (a.c <= 8192) launch_norm_as<T, kVe, 256, 32, P>(a, parts);
-        else if (a.c <= 16384) launch_norm_as<T, kVe, 512, 32, P>(a, parts);
-        else launch_norm_as<T, kVe, 1024, 32, P>(a, parts);
+        if (a.c <= 64) launch_forward_as<T, kVe, 8, 8, Q8>(a);
+        else if (a.c <= 128) launch_forward_as<T, kVe, 8, 16, Q8>(a);
+        else if (a.c <= 256) launch_forward_as<T, kVe, 8, 32, Q8>(a);
+        else if (a.c <= 512) launch_forward_as<T, kVe, 32, 16, Q8>(a);
+        else if (a.c <= 1024) launch_forward_as<T, kVe, 32, 32, Q8>(a);
+        else if (a.c <= 2048) launch_forward_as<T, kVe, 128, 16, Q8>(a);
+        else if (a.c <= 4096) launch_forward_as<T, kVe, 128, 32, Q8>(a);
+        else if (a.c <= 8192) launch_forward_as<T, kVe, 256, 32, Q8>(a);
+        else if (a.c <= 16384) launch_forward_as<T, kVe, 512, 32, Q8>(a);
+        else launch_forward_as<T, kVe, 1024, 32, Q8>(a);
     } else {
-        if (a.c <= 256) launch_norm_as<T, 1, 32, 8, P>(a, parts);
-        else if (a.c <= 512) launch_norm_as<T, 1, 32, 16, P>(a, parts);
-        else if (a.c <= 1024) launch_norm_as<T, 1, 32, 32, P>(a, parts);
-        else if (a.c <= 4096) launch_norm_as<T, 1, 128, 32, P>(a, parts);
-        else launch_norm_as<T, 1, 1024, 32, P>(a, parts);
+        if (a.c <= 256) launch_forward_as<T, 1, 32, 8, Q8>(a);
+        else if (a.c <= 512) launch_forward_as<T, 1, 32, 16, Q8>(a);
+        else if (a.c <= 1024) launch_forward_as<T, 1, 32, 32, Q8>(a);
+        else if (a.c <= 4096) launch_forward_as<T, 1, 128, 32, Q8>(a);
+        else launch_forward_as<T, 1, 1024, 32, Q8>(a);
     }
 }
 
-template <NormPass P>
-void launch_norm_type(spconv_dtype_t dtype, const NormArgs& a, int* parts) {
-    if (dtype == SPCONV_BF16)
-        launch_norm<__nv_bfloat16, P>(a, parts);
-    else
-        launch_norm<float, P>(a, parts);
+// 8 elements a thread up to 4096 channels, then more.
+template <typename T>
+int launch_backward(const NormArgs& a) {
+    constexpr int kVe = 16 / (int)sizeof(T);
+    if (a.c > 32768) {
+        const int parts = row_parts(a.n, 1);
+        k_rms_norm_backward_long<T><<<parts, kLongThreads, 0, a.stream>>>(
+            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
+            static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
+        return parts;
+    }
+    if (a.c % kVe == 0) {
+        if (a.c <= 64) return launch_backward_as<T, kVe, 8, 8>(a);
+        if (a.c <= 128) return launch_backward_as<T, kVe, 16, 8>(a);
+        if (a.c <= 256) return launch_backward_as<T, kVe, 32, 8>(a);
+        if (a.c <= 512) return launch_backward_as<T, kVe, 64, 8>(a);
+        if (a.c <= 1024) return launch_backward_as<T, kVe, 128, 8>(a);
+        if (a.c <= 2048) return launch_backward_as<T, kVe, 256, 8>(a);
+        if (a.c <= 4096) return launch_backward_as<T, kVe, 512, 8>(a);
+        if (a.c <= 8192) return launch_backward_as<T, kVe, 512, 16>(a);
+        if (a.c <= 16384) return launch_backward_as<T, kVe, 512, 32>(a);
+        return launch_backward_as<T, kVe, 1024, 32>(a);
+    }
+    if (a.c <= 256) return launch_backward_as<T, 1, 32, 8>(a);
+    if (a.c <= 1024) return launch_backward_as<T, 1, 128, 8>(a);
+    if (a.c <= 4096) return launch_backward_as<T, 1, 512, 8>(a);
+    return launch_backward_as<T, 1, 1024, 32>(a);
 }
 
 spconv_status_t norm_args(spconv_dtype_t dtype, const void* x, const void* residual, const void* weight, int64_t n,
@@ -472,7 +534,10 @@ spconv_status_t spconv_rms_norm(spconv_dtype_t dtype, const void* x, const void*
         return row_fail(SPCONV_ERR_INVALID_ARG, "out and rstd must not overlap another buffer of the call");
     NormArgs a = {x, residual, weight, n, channels, eps, sum_out, out, rstd};
     a.stream = static_cast<cudaStream_t>(stream);
-    launch_norm_type<NormPass::kRows>(dtype, a, nullptr);
+    if (dtype == SPCONV_BF16)
+        launch_forward<__nv_bfloat16, false>(a);
+    else
+        launch_forward<float, false>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm");
 }
@@ -491,7 +556,10 @@ spconv_status_t spconv_rms_norm_q8(spconv_dtype_t dtype, const void* x, const vo
         return row_fail(SPCONV_ERR_INVALID_ARG, "q and scale must not overlap another buffer of the call");
     NormArgs a = {x, residual, weight, n, channels, eps, sum_out, nullptr, nullptr, q, scale};
     a.stream = static_cast<cudaStream_t>(stream);
-    launch_norm_type<NormPass::kQ8>(dtype, a, nullptr);
+    if (dtype == SPCONV_BF16)
+        launch_forward<__nv_bfloat16, true>(a);
+    else
+        launch_forward<float, true>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm_q8");
 }
@@ -547,10 +615,9 @@ spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, c
     a.dx = dx;
     a.part = dweight ? static_cast<float*>(workspace) : nullptr;
     a.stream = st;
-    int parts = 0;
-    launch_norm_type<NormPass::kBackward>(dtype, a, &parts);
-    if (dweight) k_rms_norm_dw<<<(channels + 31) / 32, 256, 0, st>>>(a.part, parts, channels, dweight);
-    const cudaError_t e = cudaGetLastError();
+    const int parts = dtype == SPCONV_BF16 ? launch_backward<__nv_bfloat16>(a) : launch_backward<float>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && dweight) e = launch_dw(a.part, parts, channels, dweight, st);
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm_backward");
 }
 

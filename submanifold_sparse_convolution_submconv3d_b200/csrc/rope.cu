@@ -146,17 +146,18 @@ void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cud
     const int sms = device_sms();
     a.chunks = a.pairs / (HALVES ? VE : VE / 2);
     const int per_voxel = a.heads * a.chunks;  // <= 65535 * 128
-    // Items a unit: four loads a lane keep the memory busy; where that leaves warps
-    // without work, one load a lane spreads a short call over more of them.
+    // Items a unit: four loads a lane in flight at once keep the memory busy; where that
+    // leaves warps without work, one load a lane spreads a short call over more of them.
     const int full = HALVES ? 64 : 128;
     const int want = a.n * per_voxel >= (int64_t)sms * 32 * full ? full : 32;
     a.voxels = 1;
     a.unit_heads = a.heads;
     if (per_voxel < want) {
-        a.voxels = (want + per_voxel - 1) / per_voxel;
+        a.voxels = want / per_voxel;
         if (a.voxels * a.pairs > kRopeTable) a.voxels = kRopeTable / a.pairs;
-    } else if (per_voxel >= 2 * want) {
-        a.unit_heads = (want + a.chunks - 1) / a.chunks;
+    } else {
+        const int groups = (per_voxel + want - 1) / want;
+        a.unit_heads = (a.heads + groups - 1) / groups;
     }
     a.head_groups = (a.heads + a.unit_heads - 1) / a.unit_heads;
     a.units = (a.n + a.voxels - 1) / a.voxels * a.head_groups;
