@@ -44,54 +44,68 @@ __device__ __forceinline__ uint32_t codes(uint32_t w, int i, __half) {
     return bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1032.0f)));
 }
 
-// Eight neighbouring elements of a row of x as the pairs (x0, x4), (x1, x5), (x2, x6),
-// (x3, x7) that meet the codes of a word, in PARTS 16-bit floats each whose sum is x.
-template <typename X>
-struct XWord;
-template <>
-struct XWord<__nv_bfloat16> {
+// A lane's share of a group of a row of x: W words of 8 neighbouring elements, each word
+// as the pairs (x0, x4), (x1, x5), (x2, x6), (x3, x7) that meet the codes of a word, in
+// kParts 16-bit floats each whose sum is x.
+template <typename X, int W>
+struct XShare;
+template <int W>
+struct XShare<__nv_bfloat16, W> {
     using Half = __nv_bfloat16;
     static constexpr int kParts = 1;
-    uint4 v;
-    __device__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-    __device__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ uint32_t pair(int i, int) const {
-        return __byte_perm(i < 2 ? v.x : v.y, i < 2 ? v.z : v.w, i & 1 ? 0x7632 : 0x5410);
+    uint4 v[W];
+    __device__ void load(const __nv_bfloat16* p, bool in) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) v[w] = in ? reinterpret_cast<const uint4*>(p)[w] : make_uint4(0, 0, 0, 0);
+    }
+    __device__ uint32_t pair(int w, int i, int) const {
+        return __byte_perm(i < 2 ? v[w].x : v[w].y, i < 2 ? v[w].z : v[w].w, i & 1 ? 0x7632 : 0x5410);
     }
 };
-template <>
-struct XWord<__nv_fp8_e4m3> {
+template <int W>
+struct XShare<__nv_fp8_e4m3, W> {
     using Half = __half;  // holds every e4m3 value
     static constexpr int kParts = 1;
-    uint2 v;
-    __device__ void load(const __nv_fp8_e4m3* p) { v = *reinterpret_cast<const uint2*>(p); }
-    __device__ void zero() { v = make_uint2(0, 0); }
-    __device__ uint32_t pair(int i, int) const {
-        const uint32_t two = __byte_perm(v.x, v.y, i | ((i + 4) << 4));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-        return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    uint32_t v[2 * W];
+    __device__ void load(const __nv_fp8_e4m3* p, bool in) {
+        if (W % 2 == 0) {
+#pragma unroll
+            for (int w = 0; w < W / 2; ++w) {
+                const uint4 u = in ? reinterpret_cast<const uint4*>(p)[w] : make_uint4(0, 0, 0, 0);
+                v[4 * w] = u.x, v[4 * w + 1] = u.y, v[(4 * w + 2) % (2 * W)] = u.z, v[(4 * w + 3) % (2 * W)] = u.w;
+            }
+        } else {
+            const uint2 u = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
+            v[0] = u.x, v[1] = u.y;
+        }
+    }
+    __device__ uint32_t pair(int w, int i, int) const {
+        const uint32_t two = __byte_perm(v[2 * w], v[2 * w + 1], i | ((i + 4) << 4));
+        uint32_t r;
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+        return r;
     }
 };
-template <>
-struct XWord<float> {
+template <int W>
+struct XShare<float, W> {
     // Three bf16 parts, each the leading 8 bits (cut, so the next is exact): 24 bits in all.
     using Half = __nv_bfloat16;
     static constexpr int kParts = 3;
-    float v[8];
-    __device__ void load(const float* p) {
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
-        *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(p + 4);
-    }
-    __device__ void zero() {
+    float v[8 * W];
+    __device__ void load(const float* p, bool in) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        for (int w = 0; w < 2 * W; ++w)
+            *reinterpret_cast<float4*>(v + 4 * w) =
+                in ? reinterpret_cast<const float4*>(p)[w] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     __device__ static uint32_t part_of(float x, int part) {
         if (!(fabsf(x) <= 3.402823466e38f)) return part == 0 ? (x != x ? 0x7fc0u : __float_as_uint(x) >> 16) : 0u;
         for (int k = 0; k < part; ++k) x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
         return __float_as_uint(x) >> 16;
     }
-    __device__ uint32_t pair(int i, int part) const { return part_of(v[i], part) | (part_of(v[i + 4], part) << 16); }
+    __device__ uint32_t pair(int w, int i, int part) const {
+        return part_of(v[8 * w + i], part) | (part_of(v[8 * w + i + 4], part) << 16);
+    }
 };
 
 template <typename Half>
@@ -102,8 +116,24 @@ struct Ones {
 constexpr int kW4Warps = 8;
 constexpr int kW4Chunk = 128;  // input channels a warp takes at a time: 16 codes words a row
 
-// A warp multiplies 16 MT outputs by 8 NT rows over every kW4Warps-th chunk; the warps'
-// sums are joined in shared memory.
+constexpr int kW4Segment = 128;  // groups whose scales a CTA holds in shared memory
+
+// A scale and its offset side by side, read with one access.
+template <typename T>
+struct alignas(2 * sizeof(T)) ScaleOffset {
+    T s, z;
+};
+
+template <typename T, int MT, int NT>
+constexpr int kW4Join = kW4Warps * MT * 16 * (NT * 8 + 1) * 4;
+template <typename T, int MT, int NT>
+inline int w4_smem(int groups) {
+    const int table = (groups < kW4Segment ? groups : kW4Segment) * MT * 16 * (int)sizeof(ScaleOffset<T>);
+    return table > kW4Join<T, MT, NT> ? table : kW4Join<T, MT, NT>;
+}
+
+// A CTA multiplies 16 MT outputs by 8 NT rows; a warp takes every kW4Warps-th chunk of
+// the input channels, and the warps' sums are joined in shared memory.
 //
 // Fragments.  In one 16 x 8 x 16 step lane (g, t) = (lane / 4, lane % 4) holds four
 // input channels of outputs g and g + 8 and of row g; which four is free as long as both
@@ -113,18 +143,22 @@ constexpr int kW4Chunk = 128;  // input channels a warp takes at a time: 16 code
 //
 // Scales.  Over a group, with q' = q - 8:  sum w x = s sum q' x + (z + 8 s) sum x; the
 // first sum is the step's accumulator, started at zero for each group, the second comes
-// out of the same instruction with ones in place of the codes.
+// out of the same instruction with ones in place of the codes.  The scales of the
+// CTA's outputs are brought into shared memory along the groups, as they lie in memory;
+// read per lane from global memory, each of them would cost a cache line's lookup.
 template <typename T, typename X, int MT, int NT, int GROUP>
 __global__ void __launch_bounds__(32 * kW4Warps)
     k_linear_w4(const X* __restrict__ x, const float* __restrict__ x_scale, int n, int cin,
                 const uint32_t* __restrict__ packed, const T* __restrict__ scales, const T* __restrict__ offsets,
                 const T* __restrict__ bias, T* __restrict__ out, int cout) {
-    using Half = typename XWord<X>::Half;
-    constexpr int kParts = XWord<X>::kParts;
-    constexpr int kW = GROUP / 32, kGroups = kW4Chunk / GROUP;
-    __shared__ float join[kW4Warps][MT * 16][NT * 8 + 1];
+    constexpr int kW = GROUP / 32, kGroups = kW4Chunk / GROUP, kOut = MT * 16, kThreads = 32 * kW4Warps;
+    using Share = XShare<X, kW>;
+    using Half = typename Share::Half;
+    constexpr int kParts = Share::kParts;
+    extern __shared__ __align__(16) unsigned char smem[];
+    ScaleOffset<T>* table = reinterpret_cast<ScaleOffset<T>*>(smem);  // [group of the segment][output]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int o0 = blockIdx.x * MT * 16, row0 = blockIdx.y * NT * 8;
+    const int o0 = blockIdx.x * kOut, row0 = blockIdx.y * NT * 8;
     const int words = cin / 8, groups = cin / GROUP;
     float y[MT][NT][4];
 #pragma unroll
@@ -133,10 +167,10 @@ __global__ void __launch_bounds__(32 * kW4Warps)
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[m][b][e] = 0.0f;
-    for (int k0 = warp * kGroups; k0 < groups; k0 += kW4Warps * kGroups) {
-        // the chunk's codes, scales and offsets
-        uint32_t w[MT][2][kGroups][kW];
-        float s[MT][2][kGroups], z[MT][2][kGroups];
+
+    // A chunk's codes: [output half][group][word]
+    uint32_t w[MT][2][kGroups][kW];
+    const auto fetch = [&](int k0) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -147,74 +181,93 @@ __global__ void __launch_bounds__(32 * kW4Warps)
                     const bool in = o < cout && k0 + j < groups;
                     const uint32_t* p = packed + (int64_t)o * words + (k0 + j) * (GROUP / 8) + t * kW;
                     if (kW == 4) {
-                        const uint4 v = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-                        w[m][r][j][0] = v.x, w[m][r][j][kW > 1 ? 1 : 0] = v.y;
-                        w[m][r][j][kW > 2 ? 2 : 0] = v.z, w[m][r][j][kW > 2 ? 3 : 0] = v.w;
+                        const uint4 v = in ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+                        w[m][r][j][0] = v.x, w[m][r][j][1 % kW] = v.y, w[m][r][j][2 % kW] = v.z, w[m][r][j][3 % kW] = v.w;
                     } else if (kW == 2) {
-                        const uint2 v = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
-                        w[m][r][j][0] = v.x, w[m][r][j][kW > 1 ? 1 : 0] = v.y;
+                        const uint2 v = in ? __ldcs(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+                        w[m][r][j][0] = v.x, w[m][r][j][1 % kW] = v.y;
                     } else {
                         w[m][r][j][0] = in ? *p : 0;
                     }
-                    const int64_t at = (int64_t)o * groups + k0 + j;
-                    s[m][r][j] = in ? to_f32(scales[at]) : 0.0f;
-                    z[m][r][j] = in ? to_f32(offsets[at]) : 0.0f;
                 }
             }
+    };
+    for (int seg = 0; seg < groups; seg += kW4Segment) {
+        const int seg_end = min(groups, seg + kW4Segment), held = seg_end - seg;
+        fetch(seg + warp * kGroups);
+        if (seg) __syncthreads();
+        for (int e = threadIdx.x; e < held * kOut; e += kThreads) {
+            const int o = e / held, k = e - o * held;
+            ScaleOffset<T> v;
+            v.s = v.z = from_f32<T>(0.0f);
+            if (o0 + o < cout) {
+                const int64_t at = (int64_t)(o0 + o) * groups + seg + k;
+                v.s = scales[at];
+                v.z = offsets[at];
+            }
+            table[k * kOut + o] = v;
+        }
+        __syncthreads();
+        for (int k0 = seg + warp * kGroups; k0 < seg_end; k0 += kW4Warps * kGroups) {
+            if (k0 != seg + warp * kGroups) fetch(k0);
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            float d[MT][NT][4], sum[NT][4];
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sum[b][e] = 0.0f;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) d[m][b][e] = 0.0f;
-                }
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                XWord<X> xw[NT];
+            for (int j = 0; j < kGroups; ++j) {
+                Share xs[NT];
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
                     const int row = row0 + b * 8 + g;
-                    xw[b].zero();
-                    if (row < n && k0 + j < groups)
-                        xw[b].load(x + (int64_t)row * cin + (k0 + j) * GROUP + (t * kW + i) * 8);
+                    xs[b].load(x + (int64_t)row * cin + (k0 + j) * GROUP + t * kW * 8, row < n && k0 + j < groups);
                 }
+                float d[MT][NT][4], sum[NT][4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sum[b][e] = 0.0f;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) d[m][b][e] = 0.0f;
+                    }
+#pragma unroll
+                for (int i = 0; i < 2 * kW; ++i) {
                     uint32_t a[MT][4];
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        a[m][0] = codes(w[m][0][j][i], 2 * half, Half());
-                        a[m][1] = codes(w[m][1][j][i], 2 * half, Half());
-                        a[m][2] = codes(w[m][0][j][i], 2 * half + 1, Half());
-                        a[m][3] = codes(w[m][1][j][i], 2 * half + 1, Half());
+                        a[m][0] = codes(w[m][0][j][i / 2], i % 2 * 2, Half());
+                        a[m][1] = codes(w[m][1][j][i / 2], i % 2 * 2, Half());
+                        a[m][2] = codes(w[m][0][j][i / 2], i % 2 * 2 + 1, Half());
+                        a[m][3] = codes(w[m][1][j][i / 2], i % 2 * 2 + 1, Half());
                     }
                     const uint32_t ones[4] = {Ones<Half>::v, Ones<Half>::v, Ones<Half>::v, Ones<Half>::v};
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
 #pragma unroll
                         for (int b = 0; b < NT; ++b) {
-                            const uint32_t b0 = xw[b].pair(2 * half, p), b1 = xw[b].pair(2 * half + 1, p);
+                            const uint32_t b0 = xs[b].pair(i / 2, i % 2 * 2, p), b1 = xs[b].pair(i / 2, i % 2 * 2 + 1, p);
                             mma_16816(sum[b], ones, b0, b1, Half());
 #pragma unroll
                             for (int m = 0; m < MT; ++m) mma_16816(d[m][b], a[m], b0, b1, Half());
                         }
                 }
-            }
+                if (k0 + j >= seg_end) continue;  // behind the last group: zeros so far, and no scale
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int b = 0; b < NT; ++b)
+                    for (int r = 0; r < 2; ++r) {
+                        const ScaleOffset<T> v = table[(k0 + j - seg) * kOut + m * 16 + r * 8 + g];
+                        const float sc = to_f32(v.s), of = fmaf(8.0f, sc, to_f32(v.z));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float sc = s[m][e >> 1][j], of = fmaf(8.0f, sc, z[m][e >> 1][j]);
-                        y[m][b][e] = fmaf(sc, d[m][b][e], fmaf(of, sum[b][e & 1], y[m][b][e]));
+                        for (int b = 0; b < NT; ++b)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float& to = y[m][b][2 * r + e];
+                                to = fmaf(sc, d[m][b][2 * r + e], fmaf(of, sum[b][e], to));
+                            }
                     }
+            }
         }
     }
+    __syncthreads();
+    float (*join)[kOut][NT * 8 + 1] = reinterpret_cast<float (*)[kOut][NT * 8 + 1]>(smem);
     // accumulator e of lane (g, t): output g + 8 (e / 2), row 2 t + e % 2
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -223,8 +276,8 @@ __global__ void __launch_bounds__(32 * kW4Warps)
 #pragma unroll
             for (int e = 0; e < 4; ++e) join[warp][m * 16 + (e >> 1) * 8 + g][b * 8 + 2 * t + (e & 1)] = y[m][b][e];
     __syncthreads();
-    for (int at = threadIdx.x; at < MT * 16 * NT * 8; at += 32 * kW4Warps) {
-        const int o = at % (MT * 16), r = at / (MT * 16);
+    for (int at = threadIdx.x; at < kOut * NT * 8; at += kThreads) {
+        const int o = at % kOut, r = at / kOut;
         if (o0 + o >= cout || row0 + r >= n) continue;
         float v = 0.0f;
 #pragma unroll
@@ -302,36 +355,62 @@ spconv_status_t w4_args(spconv_dtype_t dtype, const void* packed, const void* sc
     return SPCONV_OK;
 }
 
+struct W4Args {
+    const void* x;
+    const float* x_scale;
+    int n, cin;
+    const void *packed, *scales, *offsets, *bias;
+    void* out;
+    int cout;
+    cudaStream_t stream;
+};
+
 template <typename T, typename X, int MT, int NT, int GROUP>
-void launch_w4_as(const void* x, const float* x_scale, int n, int cin, const void* packed, const void* scales,
-                  const void* offsets, const void* bias, void* out, int cout, cudaStream_t st) {
-    const dim3 grid((cout + 16 * MT - 1) / (16 * MT), (n + 8 * NT - 1) / (8 * NT));
-    k_linear_w4<T, X, MT, NT, GROUP><<<grid, 32 * kW4Warps, 0, st>>>(
-        static_cast<const X*>(x), x_scale, n, cin, static_cast<const uint32_t*>(packed), static_cast<const T*>(scales),
-        static_cast<const T*>(offsets), static_cast<const T*>(bias), static_cast<T*>(out), cout);
+void launch_w4_as(const W4Args& a) {
+    const dim3 grid((a.cout + 16 * MT - 1) / (16 * MT), (a.n + 8 * NT - 1) / (8 * NT));
+    const int smem = w4_smem<T, MT, NT>(a.cin / GROUP);
+    if (smem > 48 * 1024)
+        cudaFuncSetAttribute(k_linear_w4<T, X, MT, NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    k_linear_w4<T, X, MT, NT, GROUP><<<grid, 32 * kW4Warps, smem, a.stream>>>(
+        static_cast<const X*>(a.x), a.x_scale, a.n, a.cin, static_cast<const uint32_t*>(a.packed),
+        static_cast<const T*>(a.scales), static_cast<const T*>(a.offsets), static_cast<const T*>(a.bias),
+        static_cast<T*>(a.out), a.cout);
 }
 
+// Outputs a CTA: many of them share one read and conversion of x, as long as every SM
+// still gets a CTA.
+template <typename T, typename X, int NT, int GROUP, int MOST>
+void launch_w4_rows(const W4Args& a) {
+    constexpr int kSms = 148;
+    if (MOST >= 4 && a.cout >= 64 * kSms)
+        launch_w4_as<T, X, MOST < 4 ? 1 : 4, NT, GROUP>(a);
+    else if (MOST >= 2 && a.cout >= 32 * kSms)
+        launch_w4_as<T, X, MOST < 2 ? 1 : 2, NT, GROUP>(a);
+    else
+        launch_w4_as<T, X, 1, NT, GROUP>(a);
+}
+
+// Rows a CTA: all of them, so that the weights are read once; fp32 rows take three
+// times the registers, and go 16 at a time.
 template <typename T, typename X, int GROUP>
-void launch_w4_group(const void* x, const float* x_scale, int n, int cin, const void* packed, const void* scales,
-                     const void* offsets, const void* bias, void* out, int cout, cudaStream_t st) {
-    if (n <= 8) {
-        launch_w4_as<T, X, 1, 1, GROUP>(x, x_scale, n, cin, packed, scales, offsets, bias, out, cout, st);
-    } else if (n <= 16 || sizeof(X) == 4) {  // fp32 rows take three times the registers
-        launch_w4_as<T, X, 1, 2, GROUP>(x, x_scale, n, cin, packed, scales, offsets, bias, out, cout, st);
+void launch_w4_group(const W4Args& a) {
+    if (a.n <= 8) {
+        launch_w4_rows<T, X, 1, GROUP, sizeof(X) == 4 ? 2 : 4>(a);
+    } else if (a.n <= 16 || sizeof(X) == 4) {
+        launch_w4_rows<T, X, 2, GROUP, sizeof(X) == 4 ? 1 : 2>(a);
     } else if constexpr (sizeof(X) < 4) {
-        launch_w4_as<T, X, 2, 4, GROUP>(x, x_scale, n, cin, packed, scales, offsets, bias, out, cout, st);
+        launch_w4_rows<T, X, 4, GROUP, 2>(a);
     }
 }
 
 template <typename T, typename X>
-void launch_linear_w4(const void* x, const float* x_scale, int64_t n, int cin, const void* packed, const void* scales,
-                      const void* offsets, int group, const void* bias, void* out, int cout, cudaStream_t st) {
+void launch_linear_w4(const W4Args& a, int group) {
     if (group == 32)
-        launch_w4_group<T, X, 32>(x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, st);
+        launch_w4_group<T, X, 32>(a);
     else if (group == 64)
-        launch_w4_group<T, X, 64>(x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, st);
+        launch_w4_group<T, X, 64>(a);
     else
-        launch_w4_group<T, X, 128>(x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, st);
+        launch_w4_group<T, X, 128>(a);
 }
 
 }  // namespace
@@ -406,16 +485,15 @@ spconv_status_t spconv_linear_w4(spconv_dtype_t dtype, const void* x, const floa
         overlaps(out, ob, packed, pb) || overlaps(out, ob, scales, gb) || overlaps(out, ob, offsets, gb) ||
         overlaps(out, ob, bias, (int64_t)cout * es))
         return row_fail(SPCONV_ERR_INVALID_ARG, "out must not overlap another buffer of the call");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const W4Args a = {x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, static_cast<cudaStream_t>(stream)};
     if (dtype == SPCONV_BF16 && x_scale)
-        launch_linear_w4<__nv_bfloat16, __nv_fp8_e4m3>(x, x_scale, n, cin, packed, scales, offsets, group, bias, out, cout, st);
+        launch_linear_w4<__nv_bfloat16, __nv_fp8_e4m3>(a, group);
     else if (dtype == SPCONV_BF16)
-        launch_linear_w4<__nv_bfloat16, __nv_bfloat16>(x, nullptr, n, cin, packed, scales, offsets, group, bias, out,
-                                                       cout, st);
+        launch_linear_w4<__nv_bfloat16, __nv_bfloat16>(a, group);
     else if (x_scale)
-        launch_linear_w4<float, __nv_fp8_e4m3>(x, x_scale, n, cin, packed, scales, offsets, group, bias, out, cout, st);
+        launch_linear_w4<float, __nv_fp8_e4m3>(a, group);
     else
-        launch_linear_w4<float, float>(x, nullptr, n, cin, packed, scales, offsets, group, bias, out, cout, st);
+        launch_linear_w4<float, float>(a, group);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_linear_w4");
 }

@@ -233,68 +233,117 @@ __device__ __forceinline__ float group_sum(float v, float* part, int group) {
     return v;
 }
 
+// Rows of the gradient a thread fetches ahead, in shared memory (16-byte copies of its
+// own elements, so no thread waits for another).
+constexpr int kAhead = 2, kStages = kAhead + 1;
+template <typename T, int VE, int E>
+constexpr bool kFetchesAhead = VE * sizeof(T) == 16 && E * sizeof(T) <= 32;
+template <typename T, int VE, int TPR, int E>
+constexpr int kBackwardSmem =
+    kFetchesAhead<T, VE, E> ? kStages * 3 * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512) : 0;
+
+__device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+
 // dx of the rows and, in `part`, each CTA's column sums of dy * xh.  A CTA's row groups
 // of TPR threads take rows blockIdx.x * kRows + group, and so on by gridDim.x * kRows,
 // and wait only within the group; a thread keeps the sums of its columns in registers
 // over all its rows, and the groups' sums are joined in shared memory at the end.
-// Few elements a thread (E = 8 up to 4096 channels) leave room for 32 warps an SM,
-// whose loads cover each other's reductions.
 template <typename T, int VE, int TPR, int E>
-__global__ void __launch_bounds__(TPR > 512 ? TPR : 512, E == 8 ? 2 : 1)
+__global__ void __launch_bounds__(TPR > 512 ? TPR : 512, E == 8 && sizeof(T) == 2 ? 2 : 1)
     k_rms_norm_backward(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
                         const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
                         float* __restrict__ part) {
+    using V = Vec<T, VE>;
     constexpr int kThreads = TPR > 512 ? TPR : 512, kRows = kThreads / TPR, kItems = E / VE;
+    constexpr bool kFetch = kFetchesAhead<T, VE, E>;
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    V* ring = reinterpret_cast<V*>(ring_bytes) + threadIdx.x;  // [stage][dy, h, dsum][item][thread]
     __shared__ float red[2][kThreads / 32];
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     float dw[E];
+    V w[kItems];
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int j = (k * TPR + t) * VE;
+        if (weight && j < c) w[k] = load<T, VE>(weight + j);
+    }
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t i = (int64_t)blockIdx.x * kRows + group;
+    const auto fetch = [&](int64_t row, int stage) {
+        V* to = ring + stage * (3 * kItems * kThreads);
+        if (row < n) {
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int j = (k * TPR + t) * VE;
+                if (j >= c) continue;
+                copy_ahead(to + k * kThreads, dy + row * c + j);
+                copy_ahead(to + (kItems + k) * kThreads, h + row * c + j);
+                if (dsum) copy_ahead(to + (2 * kItems + k) * kThreads, dsum + row * c + j);
+            }
+        }
+        copies_group();
+    };
+    if (kFetch) {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) fetch(i + a * step, a);
+    }
+    float rstd_next = i < n ? rstd_in[i] : 0.0f;
     int turn = 0;  // the sums' buffer: a thread may still read the last row's
-    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += (int64_t)gridDim.x * kRows, turn ^= 1) {
-        const int64_t i = i0 + group;
+    int stage = 0;
+    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += step, i += step, turn ^= 1) {
         const bool live = i < n;
-        const int64_t base = i * c;
-        Vec<T, VE> vd[kItems], vh[kItems], vs[kItems];
+        const float rstd = rstd_next;
+        rstd_next = i + step < n ? rstd_in[i + step] : 0.0f;
+        V vd[kItems], vh[kItems], vs[kItems];
+        const V* from = ring + stage * (3 * kItems * kThreads);
+        if (kFetch) copies_wait();
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int j = (k * TPR + t) * VE;
             if (live && j < c) {
-                vd[k] = load<T, VE>(dy + base + j);
-                vh[k] = load<T, VE>(h + base + j);
-                if (dsum) vs[k] = load<T, VE>(dsum + base + j);
+                vd[k] = kFetch ? from[k * kThreads] : load<T, VE>(dy + i * c + j);
+                vh[k] = kFetch ? from[(kItems + k) * kThreads] : load<T, VE>(h + i * c + j);
+                if (dsum) vs[k] = kFetch ? from[(2 * kItems + k) * kThreads] : load<T, VE>(dsum + i * c + j);
             }
         }
-        const float rstd = live ? rstd_in[i] : 0.0f;
-        float dot = 0.0f;
+        float g[E], xh[E], dot = 0.0f;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int j = (k * TPR + t) * VE;
-            if (!live || j >= c) continue;
-            Vec<T, VE> w;
-            if (weight) w = load<T, VE>(weight + j);
+            if (!live || (k * TPR + t) * VE >= c) continue;
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float dxh = to_f32(vd[k].v[e]) * (to_f32(vh[k].v[e]) * rstd);
-                dw[k * VE + e] += dxh;
-                dot += dxh * (weight ? to_f32(w.v[e]) : 1.0f);
+                const int at = k * VE + e;
+                const float d = to_f32(vd[k].v[e]);
+                xh[at] = to_f32(vh[k].v[e]) * rstd;
+                g[at] = weight ? d * to_f32(w[k].v[e]) : d;
+                dw[at] = fmaf(d, xh[at], dw[at]);
+                dot = fmaf(g[at], xh[at], dot);
             }
+        }
+        if (kFetch) {
+            // into the stage read in the last turn
+            fetch(i + kAhead * step, stage == 0 ? kStages - 1 : stage - 1);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
         }
         const float mean = group_sum<TPR>(dot, red[turn], group) / (float)c;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int j = (k * TPR + t) * VE;
             if (!live || j >= c) continue;
-            Vec<T, VE> w, o;
-            if (weight) w = load<T, VE>(weight + j);
+            V o;
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float g = to_f32(vd[k].v[e]) * (weight ? to_f32(w.v[e]) : 1.0f);
-                float d = rstd * (g - to_f32(vh[k].v[e]) * rstd * mean);
-                if (dsum) d += to_f32(vs[k].v[e]);
-                o.v[e] = from_f32<T>(d);
+                const int at = k * VE + e;
+                o.v[e] = from_f32<T>(fmaf(rstd, fmaf(-xh[at], mean, g[at]), dsum ? to_f32(vs[k].v[e]) : 0.0f));
             }
-            *reinterpret_cast<Vec<T, VE>*>(dx + base + j) = o;
+            *reinterpret_cast<V*>(dx + i * c + j) = o;
         }
     }
     if (!part) return;
@@ -425,8 +474,11 @@ void launch_forward_as(const NormArgs& a) {
 template <typename T, int VE, int TPR, int E>
 int launch_backward_as(const NormArgs& a) {
     constexpr int kThreads = TPR > 512 ? TPR : 512;
+    constexpr int kSmem = kBackwardSmem<T, VE, TPR, E>;
     const int parts = row_parts(a.n, kThreads / TPR);
-    k_rms_norm_backward<T, VE, TPR, E><<<parts, kThreads, 0, a.stream>>>(
+    if (kSmem > 48 * 1024 - 16640)  // with the static arrays over what a launch has without asking
+        cudaFuncSetAttribute(k_rms_norm_backward<T, VE, TPR, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    k_rms_norm_backward<T, VE, TPR, E><<<parts, kThreads, kSmem, a.stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
         static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
     return parts;

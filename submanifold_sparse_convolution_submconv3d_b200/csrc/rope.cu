@@ -28,16 +28,13 @@ struct RopeArgs {
     int64_t n, x_row, x_head, o_row, o_head;
     int heads, pairs;
     int chunks;         // items a head
-    int voxels;         // voxels a unit
-    int unit_heads;     // heads a unit (all of them where a unit has several voxels)
-    int head_groups;    // units a voxel (1 where a unit has several voxels)
-    int64_t units;
-    uint32_t by_chunks, by_voxel, by_pairs;  // ceil(2^32 / d), for division by d
+    int chunk_blocks;   // blocks of 32 items a head
+    int lanes_head;     // lanes on a head: the items of a chunk block, at most 32
+    int head_slots;     // heads that a warp turns side by side
+    int voxel_slots;    // voxels that a warp turns side by side
+    int unit_heads;     // heads a warp turns of each of its voxels
     float sign;         // -1: turn back
 };
-
-// id / d for id * d < 2^32, with m = ceil(2^32 / d) (d = 1 wraps to 0)
-__device__ __forceinline__ int fast_div(int id, uint32_t m) { return m ? (int)__umulhi((uint32_t)id, m) : id; }
 
 // An item's elements: one 16-byte access, or single elements at any address.
 template <typename T, int VE>
@@ -45,89 +42,88 @@ struct alignas(sizeof(T) * VE == 16 ? 16 : sizeof(T)) Vec {
     T v[VE];
 };
 
-constexpr int kRopeWarps = 8;
-constexpr int kRopeTable = 512;   // cosines and sines a unit may hold
+constexpr int kRopeThreads = 256;
 
 // Items: VE neighbouring elements of a head (VE / 2 pairs) in the interleaved layout,
-// VE elements of either half (VE pairs) in the halves layout.  A warp takes a unit of
-// `voxels` voxels x `unit_heads` heads: it starts the loads of its first items, computes
-// the unit's cosines and sines once, a pair a lane, into shared memory, and turns the
-// items from there, so the sine's cost is shared by all heads of a voxel.
+// VE elements of either half (VE pairs) in the halves layout.
+//
+// A lane owns one item position of the head for the whole launch, so the cosines and
+// sines of its pairs are computed once a voxel and used for all of the voxel's heads
+// that the warp turns: head_slots heads (and, where a voxel has few heads, voxel_slots
+// voxels) side by side, kInFlight of them one after the other with their loads issued
+// before the sines.  Warps go from voxel to voxel, the next coordinates loaded ahead.
+// blockIdx.y: the block of items and the group of heads.
 template <typename T, int VE, bool HALVES>
-__global__ void __launch_bounds__(32 * kRopeWarps)
+__global__ void __launch_bounds__(kRopeThreads)
     k_rope(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a, const T* x, T* out) {
     constexpr int kPairs = HALVES ? VE : VE / 2;  // pairs an item
     constexpr int kInFlight = HALVES ? 2 : 4;
     using V = Vec<T, VE>;
     __shared__ uint64_t turn[kMaxPairs];
-    __shared__ int axis[kMaxPairs];
-    __shared__ float2 table[kRopeWarps][kRopeTable];
-    for (int j = threadIdx.x; j < a.pairs; j += blockDim.x) {
-        turn[j] = tab.turn[j];
-        axis[j] = tab.axis[j];
-    }
+    for (int j = threadIdx.x; j < a.pairs; j += kRopeThreads) turn[j] = tab.turn[j];
     __syncthreads();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float2* cs = table[warp];
-    for (int64_t unit = (int64_t)blockIdx.x * kRopeWarps + warp; unit < a.units; unit += (int64_t)gridDim.x * kRopeWarps) {
-        const int64_t vb = a.head_groups == 1 ? unit : unit / a.head_groups;
-        const int h0 = (int)(unit - vb * a.head_groups) * a.unit_heads;
-        const int64_t i0 = vb * a.voxels;
-        const int nv = (int)min((int64_t)a.voxels, a.n - i0), nh = min(a.unit_heads, a.heads - h0);
-        const int items = nv * nh * a.chunks;
-        for (int base = lane; base - lane < items; base += 32 * kInFlight) {
+    const int lane = threadIdx.x & 31;
+    const int hg = (int)blockIdx.y / a.chunk_blocks, cb = (int)blockIdx.y - hg * a.chunk_blocks;
+    const int slot = lane / a.lanes_head, chunk = cb * 32 + lane % a.lanes_head;
+    const int vs = slot / a.head_slots;
+    const bool active = vs < a.voxel_slots && chunk < a.chunks;
+    if (!active) return;
+    const int h0 = hg * a.unit_heads + slot % a.head_slots, h_end = min(a.heads, (hg + 1) * a.unit_heads);
+    const int j0 = chunk * kPairs;
+    uint32_t axes = 0;  // two bits a pair: 0 does not turn, else the axis + 1
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) axes |= (uint32_t)(tab.axis[j0 + p] + 1) << (2 * p);
+    const int64_t step = (int64_t)gridDim.x * (kRopeThreads / 32) * a.voxel_slots;
+    int64_t i = ((int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)) * a.voxel_slots + vs;
+    const int64_t x_step = a.head_slots * a.x_head, o_step = a.head_slots * a.o_head;
+    int4 at = i < a.n ? a.coords[i] : make_int4(0, 0, 0, 0);
+    for (; i < a.n; i += step) {
+        const int4 pos = at;
+        if (i + step < a.n) at = a.coords[i + step];
+        const T* px = x + i * a.x_row + h0 * a.x_head + chunk * VE;
+        T* po = out + i * a.o_row + h0 * a.o_head + chunk * VE;
+        float cs[kPairs], sn[kPairs];
+        for (int h = h0; h < h_end; h += kInFlight * a.head_slots) {
             V lo[kInFlight], hi[HALVES ? kInFlight : 1];
-            int64_t at[kInFlight];
-            int row[kInFlight];
 #pragma unroll
             for (int k = 0; k < kInFlight; ++k) {
-                const int id = base + 32 * k;
-                if (id >= items) continue;
-                const int b = a.voxels == 1 ? 0 : fast_div(id, a.by_voxel);
-                const int r = id - b * a.heads * a.chunks;
-                const int head = fast_div(r, a.by_chunks), chunk = r - head * a.chunks;
-                const T* p = x + (i0 + b) * a.x_row + (h0 + head) * a.x_head + chunk * VE;
-                lo[k] = *reinterpret_cast<const V*>(p);
-                if (HALVES) hi[k] = *reinterpret_cast<const V*>(p + a.pairs);
-                at[k] = (i0 + b) * a.o_row + (h0 + head) * a.o_head + chunk * VE;
-                row[k] = b * a.pairs + chunk * kPairs;
+                if (h + k * a.head_slots >= h_end) continue;
+                lo[k] = *reinterpret_cast<const V*>(px + k * x_step);
+                if (HALVES) hi[HALVES ? k : 0] = *reinterpret_cast<const V*>(px + k * x_step + a.pairs);
             }
-            if (base == lane) {
-                __syncwarp();  // the last unit's readers are done
-                for (int e = lane; e < nv * a.pairs; e += 32) {
-                    const int b = a.voxels == 1 ? 0 : fast_div(e, a.by_pairs);
-                    const int j = e - b * a.pairs;
-                    const int ax = axis[j];
-                    const int pos = ax < 0 ? 0 : reinterpret_cast<const int*>(a.coords + i0 + b)[1 + ax];
-                    const int32_t frac = (int32_t)((turn[j] * (uint64_t)(int64_t)pos) >> 32);
-                    float sn, cs_;
+            px += kInFlight * x_step;
+            if (h == h0) {
+#pragma unroll
+                for (int p = 0; p < kPairs; ++p) {
+                    const uint32_t ax = (axes >> (2 * p)) & 3u;
+                    const int c = ax == 1 ? pos.y : ax == 2 ? pos.z : ax == 3 ? pos.w : 0;
+                    const int32_t frac = (int32_t)((turn[j0 + p] * (uint64_t)(int64_t)c) >> 32);
                     if (sizeof(T) == 2) {
                         // 2^-21.2 of error on [-pi, pi], against the 2^-9 of the result's rounding
                         const float ang = (float)frac * 1.46291807926715968e-9f;  // 2 pi / 2^32
-                        sn = __sinf(ang);
-                        cs_ = __cosf(ang);
+                        sn[p] = __sinf(ang) * a.sign;
+                        cs[p] = __cosf(ang);
                     } else {
-                        sincospif((float)frac * 0x1p-31f, &sn, &cs_);
+                        sincospif((float)frac * 0x1p-31f, &sn[p], &cs[p]);
+                        sn[p] *= a.sign;
                     }
-                    cs[e] = make_float2(cs_, sn * a.sign);
                 }
-                __syncwarp();
             }
 #pragma unroll
             for (int k = 0; k < kInFlight; ++k) {
-                if (base + 32 * k >= items) continue;
+                if (h + k * a.head_slots >= h_end) continue;
 #pragma unroll
                 for (int p = 0; p < kPairs; ++p) {
-                    const float2 t = cs[row[k] + p];
                     T& ra = HALVES ? lo[k].v[p] : lo[k].v[2 * p];
                     T& rb = HALVES ? hi[HALVES ? k : 0].v[p] : lo[k].v[HALVES ? 0 : 2 * p + 1];
                     const float u = to_f32(ra), v = to_f32(rb);
-                    ra = from_f32<T>(u * t.x - v * t.y);
-                    rb = from_f32<T>(u * t.y + v * t.x);
+                    ra = from_f32<T>(u * cs[p] - v * sn[p]);
+                    rb = from_f32<T>(u * sn[p] + v * cs[p]);
                 }
-                *reinterpret_cast<V*>(out + at[k]) = lo[k];
-                if (HALVES) *reinterpret_cast<V*>(out + at[k] + a.pairs) = hi[HALVES ? k : 0];
+                *reinterpret_cast<V*>(po + k * o_step) = lo[k];
+                if (HALVES) *reinterpret_cast<V*>(po + k * o_step + a.pairs) = hi[HALVES ? k : 0];
             }
+            po += kInFlight * o_step;
         }
     }
 }
@@ -139,34 +135,28 @@ int device_sms() {
     return sms;
 }
 
-uint32_t div_by(int d) { return d == 1 ? 0u : (uint32_t)(((uint64_t(1) << 32) + d - 1) / d); }
-
 template <typename T, int VE, bool HALVES>
 void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cudaStream_t st) {
+    constexpr int kInFlight = HALVES ? 2 : 4, kWarps = kRopeThreads / 32;
     const int sms = device_sms();
     a.chunks = a.pairs / (HALVES ? VE : VE / 2);
-    const int per_voxel = a.heads * a.chunks;  // <= 65535 * 128
-    // Items a unit: four loads a lane in flight at once keep the memory busy; where that
-    // leaves warps without work, one load a lane spreads a short call over more of them.
-    const int full = HALVES ? 64 : 128;
-    const int want = a.n * per_voxel >= (int64_t)sms * 32 * full ? full : 32;
-    a.voxels = 1;
-    a.unit_heads = a.heads;
-    if (per_voxel < want) {
-        a.voxels = want / per_voxel;
-        if (a.voxels * a.pairs > kRopeTable) a.voxels = kRopeTable / a.pairs;
-    } else {
-        const int groups = (per_voxel + want - 1) / want;
-        a.unit_heads = (a.heads + groups - 1) / groups;
-    }
-    a.head_groups = (a.heads + a.unit_heads - 1) / a.unit_heads;
-    a.units = (a.n + a.voxels - 1) / a.voxels * a.head_groups;
-    a.by_chunks = div_by(a.chunks);
-    a.by_voxel = div_by(per_voxel);
-    a.by_pairs = div_by(a.pairs);
-    const int64_t blocks = (a.units + kRopeWarps - 1) / kRopeWarps, most = (int64_t)sms * 6;
-    k_rope<T, VE, HALVES><<<(unsigned)(blocks < most ? blocks : most), 32 * kRopeWarps, 0, st>>>(
-        tab, a, static_cast<const T*>(x), static_cast<T*>(out));
+    a.chunk_blocks = (a.chunks + 31) / 32;
+    a.lanes_head = a.chunks < 32 ? a.chunks : 32;
+    const int slots = 32 / a.lanes_head;
+    a.head_slots = slots < a.heads ? slots : a.heads;
+    a.voxel_slots = slots / a.head_slots;
+    // Heads a warp: as many as it has in flight, so that a voxel's coordinates and sines
+    // are used often; where that leaves warps without work, one load a lane.
+    const int64_t warps = (a.n + a.voxel_slots - 1) / a.voxel_slots * a.chunk_blocks;
+    const int passes = (a.heads + a.head_slots - 1) / a.head_slots;
+    int per = passes <= 2 * kInFlight ? passes : kInFlight;
+    if (warps * ((passes + per - 1) / per) < (int64_t)sms * 2 * kWarps) per = 1;
+    a.unit_heads = per * a.head_slots;
+    const int groups = (passes + per - 1) / per;  // at most 65535: heads are
+    const int64_t blocks = (a.n + (int64_t)a.voxel_slots * kWarps - 1) / ((int64_t)a.voxel_slots * kWarps);
+    const int64_t most = ((int64_t)sms * 8 + groups * a.chunk_blocks - 1) / (groups * a.chunk_blocks);
+    k_rope<T, VE, HALVES><<<dim3((unsigned)(blocks < most ? blocks : most), groups * a.chunk_blocks), kRopeThreads, 0,
+                            st>>>(tab, a, static_cast<const T*>(x), static_cast<T*>(out));
 }
 
 // 16-byte items where every head starts on a 16-byte boundary and holds whole items,
