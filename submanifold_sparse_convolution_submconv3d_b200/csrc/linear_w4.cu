@@ -29,20 +29,46 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t bits(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
-__device__ __forceinline__ uint32_t bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
-
-// The codes i and i + 4 of a word, less 8, as two 16-bit floats.  A code placed in the
-// low mantissa bits of 128 (bf16) or 1024 (fp16) makes 128 + q or 1024 + q; taking 136 or
-// 1032 off is exact, and the sums then run on numbers of -8 .. 7.
-__device__ __forceinline__ uint32_t codes(uint32_t w, int i, __nv_bfloat16) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    return bits(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.0f)));
-}
-__device__ __forceinline__ uint32_t codes(uint32_t w, int i, __half) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u;
-    return bits(__hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(1032.0f)));
-}
+// The codes i and i + 4 of a word as two 16-bit floats, and how the sums over them are
+// read.  With f(q) what a code becomes, a group gives  sum w x = scale sum f(q) x +
+// offset sum x.
+//
+// Rows of e4m3 run in fp16, whose numbers under 2^-14 are spaced evenly: the bits of q
+// in the lowest places are q 2^-24, four places up 16 q 2^-24, so a code needs one mask
+// (and every other pair a shift); the pairs four places up meet x / 16, which fp16 holds.
+template <typename X>
+struct Codes {
+    using Half = __half;
+    static constexpr uint32_t kOne[2] = {0x3c003c00u, 0x4c004c00u};  // 1 and 16
+    __device__ static uint32_t pair(uint32_t w, int i) {
+        return (i < 2 ? w : w >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+    }
+    __device__ static float scale(float s) { return s * 16777216.0f; }
+    __device__ static float offset(float, float z) { return z; }
+};
+// Rows of bf16: q in the low mantissa bits of 128 makes 128 + q.  Its sums are rounded
+// at 2^-24 of 128 |x|, far under the 2^-9 of the result.
+template <>
+struct Codes<__nv_bfloat16> {
+    using Half = __nv_bfloat16;
+    static constexpr uint32_t kOne[2] = {0x3f803f80u, 0x3f803f80u};
+    __device__ static uint32_t pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+    __device__ static float scale(float s) { return s; }
+    __device__ static float offset(float s, float z) { return fmaf(-128.0f, s, z); }
+};
+// Rows of fp32: 136 taken off, exactly, so the sums run on -8 .. 7.
+template <>
+struct Codes<float> {
+    using Half = __nv_bfloat16;
+    static constexpr uint32_t kOne[2] = {0x3f803f80u, 0x3f803f80u};
+    __device__ static uint32_t pair(uint32_t w, int i) {
+        const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.0f));
+        return *reinterpret_cast<const uint32_t*>(&q);
+    }
+    __device__ static float scale(float s) { return s; }
+    __device__ static float offset(float s, float z) { return fmaf(8.0f, s, z); }
+};
 
 // A lane's share of a group of a row of x: W words of 8 neighbouring elements, each word
 // as the pairs (x0, x4), (x1, x5), (x2, x6), (x3, x7) that meet the codes of a word, in
@@ -51,7 +77,6 @@ template <typename X, int W>
 struct XShare;
 template <int W>
 struct XShare<__nv_bfloat16, W> {
-    using Half = __nv_bfloat16;
     static constexpr int kParts = 1;
     uint4 v[W];
     __device__ void load(const __nv_bfloat16* p, bool in) {
@@ -64,7 +89,6 @@ struct XShare<__nv_bfloat16, W> {
 };
 template <int W>
 struct XShare<__nv_fp8_e4m3, W> {
-    using Half = __half;  // holds every e4m3 value
     static constexpr int kParts = 1;
     uint32_t v[2 * W];
     __device__ void load(const __nv_fp8_e4m3* p, bool in) {
@@ -83,13 +107,16 @@ struct XShare<__nv_fp8_e4m3, W> {
         const uint32_t two = __byte_perm(v[2 * w], v[2 * w + 1], i | ((i + 4) << 4));
         uint32_t r;
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
+        if (i & 1) {  // meets 16 q
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(0.0625f));
+            r = *reinterpret_cast<const uint32_t*>(&v);
+        }
         return r;
     }
 };
 template <int W>
 struct XShare<float, W> {
     // Three bf16 parts, each the leading 8 bits (cut, so the next is exact): 24 bits in all.
-    using Half = __nv_bfloat16;
     static constexpr int kParts = 3;
     float v[8 * W];
     __device__ void load(const float* p, bool in) {
@@ -108,15 +135,10 @@ struct XShare<float, W> {
     }
 };
 
-template <typename Half>
-struct Ones {
-    static constexpr uint32_t v = std::is_same<Half, __half>::value ? 0x3c003c00u : 0x3f803f80u;
-};
-
 constexpr int kW4Warps = 8;
 constexpr int kW4Chunk = 128;  // input channels a warp takes at a time: 16 codes words a row
 
-constexpr int kW4Segment = 128;  // groups whose scales a CTA holds in shared memory
+constexpr int kW4Segment = 64;  // groups whose scales a CTA holds in shared memory
 
 // A scale and its offset side by side, read with one access.
 template <typename T>
@@ -124,12 +146,29 @@ struct alignas(2 * sizeof(T)) ScaleOffset {
     T s, z;
 };
 
-template <typename T, int MT, int NT>
-constexpr int kW4Join = kW4Warps * MT * 16 * (NT * 8 + 1) * 4;
+// Chunks of codes a warp has on the way besides the one it works on, through shared
+// memory (each thread copies its own words).
+template <int MT>
+constexpr int kW4Ahead = MT == 4 ? 1 : MT == 2 ? 2 : 3;
+
+template <int MT>
+constexpr int kW4Ring = (kW4Ahead<MT> + 1) * MT * 2 * 16 * 32 * kW4Warps;
 template <typename T, int MT, int NT>
 inline int w4_smem(int groups) {
-    const int table = (groups < kW4Segment ? groups : kW4Segment) * MT * 16 * (int)sizeof(ScaleOffset<T>);
-    return table > kW4Join<T, MT, NT> ? table : kW4Join<T, MT, NT>;
+    const int table = (groups < kW4Segment ? groups : kW4Segment) * (MT * 16 + 1) * (int)sizeof(ScaleOffset<T>);
+    const int join = kW4Warps * MT * 16 * (NT * 8 + 1) * 4, work = kW4Ring<MT> + table;
+    return work > join ? work : join;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_words(void* dst, const void* src, bool in) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    const int take = in ? BYTES : 0;  // the rest is filled with zeros
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(take) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(take)
+                     : "memory");
 }
 
 // A CTA multiplies 16 MT outputs by 8 NT rows; a warp takes every kW4Warps-th chunk of
@@ -141,22 +180,25 @@ inline int w4_smem(int groups) {
 // group's words [t W, t W + W), W = GROUP / 32, neighbouring in memory: W words of
 // either output with one load, and each word gives two steps.
 //
-// Scales.  Over a group, with q' = q - 8:  sum w x = s sum q' x + (z + 8 s) sum x; the
-// first sum is the step's accumulator, started at zero for each group, the second comes
-// out of the same instruction with ones in place of the codes.  The scales of the
-// CTA's outputs are brought into shared memory along the groups, as they lie in memory;
-// read per lane from global memory, each of them would cost a cache line's lookup.
+// Scales.  Over a group the sum of f(q) x is the step's accumulator, started at zero
+// for each group; the sum of x comes out of the same instruction with ones in place of
+// the codes.  The scales of the CTA's outputs are brought into shared memory along the
+// groups, as they lie in memory; read per lane from global memory, each of them would
+// cost a cache line's lookup.
 template <typename T, typename X, int MT, int NT, int GROUP>
 __global__ void __launch_bounds__(32 * kW4Warps)
     k_linear_w4(const X* __restrict__ x, const float* __restrict__ x_scale, int n, int cin,
                 const uint32_t* __restrict__ packed, const T* __restrict__ scales, const T* __restrict__ offsets,
                 const T* __restrict__ bias, T* __restrict__ out, int cout) {
     constexpr int kW = GROUP / 32, kGroups = kW4Chunk / GROUP, kOut = MT * 16, kThreads = 32 * kW4Warps;
+    constexpr int kAhead = kW4Ahead<MT>, kPitch = kOut + 1;
     using Share = XShare<X, kW>;
-    using Half = typename Share::Half;
+    using C = Codes<X>;
     constexpr int kParts = Share::kParts;
     extern __shared__ __align__(16) unsigned char smem[];
-    ScaleOffset<T>* table = reinterpret_cast<ScaleOffset<T>*>(smem);  // [group of the segment][output]
+    // [stage][output tile and half][4 words a lane][thread]
+    uint32_t* ring = reinterpret_cast<uint32_t*>(smem);
+    ScaleOffset<T>* table = reinterpret_cast<ScaleOffset<T>*>(smem + kW4Ring<MT>);  // [group of the segment][output]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int o0 = blockIdx.x * kOut, row0 = blockIdx.y * NT * 8;
     const int words = cin / 8, groups = cin / GROUP;
@@ -168,55 +210,70 @@ __global__ void __launch_bounds__(32 * kW4Warps)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[m][b][e] = 0.0f;
 
-    // A chunk's codes: [output half][group][word]
-    uint32_t w[MT][2][kGroups][kW];
-    const auto fetch = [&](int k0) {
+    // The words of a chunk's group j are copied together; a stage holds, per output, the
+    // groups' words one after the other: word j kW + i of the lane.
+    const uint32_t* mine = packed + (int64_t)(o0 + g) * words + t * kW;
+    const auto fetch = [&](int k0, int stage) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int o = o0 + m * 16 + r * 8 + g;
+                uint32_t* to = ring + ((stage * MT * 2 + m * 2 + r) * kThreads + threadIdx.x) * 4;
+                const bool row_in = o0 + m * 16 + r * 8 + g < cout;
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j) {
-                    const bool in = o < cout && k0 + j < groups;
-                    const uint32_t* p = packed + (int64_t)o * words + (k0 + j) * (GROUP / 8) + t * kW;
-                    if (kW == 4) {
-                        const uint4 v = in ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-                        w[m][r][j][0] = v.x, w[m][r][j][1 % kW] = v.y, w[m][r][j][2 % kW] = v.z, w[m][r][j][3 % kW] = v.w;
-                    } else if (kW == 2) {
-                        const uint2 v = in ? __ldcs(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-                        w[m][r][j][0] = v.x, w[m][r][j][1 % kW] = v.y;
-                    } else {
-                        w[m][r][j][0] = in ? *p : 0;
-                    }
+                    const bool in = row_in && k0 + j < groups;
+                    copy_words<4 * kW>(to + j * kW, in ? mine + (m * 16 + r * 8) * (int64_t)words + (k0 + j) * (GROUP / 8) : packed,
+                                       in);
                 }
             }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    constexpr int kStep = kW4Warps * kGroups;
+    int k0 = warp * kGroups, stage = 0;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) fetch(k0 + a * kStep, a);
     for (int seg = 0; seg < groups; seg += kW4Segment) {
-        const int seg_end = min(groups, seg + kW4Segment), held = seg_end - seg;
-        fetch(seg + warp * kGroups);
+        const int seg_end = min(groups, seg + kW4Segment);
         if (seg) __syncthreads();
-        for (int e = threadIdx.x; e < held * kOut; e += kThreads) {
-            const int o = e / held, k = e - o * held;
-            ScaleOffset<T> v;
-            v.s = v.z = from_f32<T>(0.0f);
-            if (o0 + o < cout) {
-                const int64_t at = (int64_t)(o0 + o) * groups + seg + k;
-                v.s = scales[at];
-                v.z = offsets[at];
+        for (int o = warp; o < kOut; o += kW4Warps)
+            for (int k = seg + lane; k < seg_end; k += 32) {
+                ScaleOffset<T> v;
+                v.s = v.z = from_f32<T>(0.0f);
+                if (o0 + o < cout) {
+                    v.s = scales[(int64_t)(o0 + o) * groups + k];
+                    v.z = offsets[(int64_t)(o0 + o) * groups + k];
+                }
+                table[(k - seg) * kPitch + o] = v;
             }
-            table[k * kOut + o] = v;
-        }
         __syncthreads();
-        for (int k0 = seg + warp * kGroups; k0 < seg_end; k0 += kW4Warps * kGroups) {
-            if (k0 != seg + warp * kGroups) fetch(k0);
+        for (; k0 < seg_end; k0 += kStep) {
+            fetch(k0 + kAhead * kStep, stage == 0 ? kAhead : stage - 1);  // the stage read in the last turn
+            Share xs[NT][kGroups];
+            if (NT == 1) {
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+                    xs[0][j].load(x + (int64_t)(row0 + g) * cin + (k0 + j) * GROUP + t * kW * 8,
+                                  row0 + g < n && k0 + j < groups);
+            }
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            uint4 w[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    w[m][r] = *reinterpret_cast<const uint4*>(
+                        ring + ((stage * MT * 2 + m * 2 + r) * kThreads + threadIdx.x) * 4);
+            stage = stage == kAhead ? 0 : stage + 1;
+            const auto word = [](const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                Share xs[NT];
+                if (NT > 1) {
 #pragma unroll
-                for (int b = 0; b < NT; ++b) {
-                    const int row = row0 + b * 8 + g;
-                    xs[b].load(x + (int64_t)row * cin + (k0 + j) * GROUP + t * kW * 8, row < n && k0 + j < groups);
+                    for (int b = 0; b < NT; ++b) {
+                        const int row = row0 + b * 8 + g;
+                        xs[b][j].load(x + (int64_t)row * cin + (k0 + j) * GROUP + t * kW * 8, row < n && k0 + j < groups);
+                    }
                 }
                 float d[MT][NT][4], sum[NT][4];
 #pragma unroll
@@ -231,21 +288,20 @@ __global__ void __launch_bounds__(32 * kW4Warps)
                 for (int i = 0; i < 2 * kW; ++i) {
                     uint32_t a[MT][4];
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        a[m][0] = codes(w[m][0][j][i / 2], i % 2 * 2, Half());
-                        a[m][1] = codes(w[m][1][j][i / 2], i % 2 * 2, Half());
-                        a[m][2] = codes(w[m][0][j][i / 2], i % 2 * 2 + 1, Half());
-                        a[m][3] = codes(w[m][1][j][i / 2], i % 2 * 2 + 1, Half());
-                    }
-                    const uint32_t ones[4] = {Ones<Half>::v, Ones<Half>::v, Ones<Half>::v, Ones<Half>::v};
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            a[m][e] = C::pair(word(w[m][e & 1], j * kW + i / 2), i % 2 * 2 + (e >> 1));
+                    const uint32_t ones[4] = {C::kOne[0], C::kOne[0], C::kOne[1], C::kOne[1]};
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
 #pragma unroll
                         for (int b = 0; b < NT; ++b) {
-                            const uint32_t b0 = xs[b].pair(i / 2, i % 2 * 2, p), b1 = xs[b].pair(i / 2, i % 2 * 2 + 1, p);
-                            mma_16816(sum[b], ones, b0, b1, Half());
+                            const uint32_t b0 = xs[b][j].pair(i / 2, i % 2 * 2, p);
+                            const uint32_t b1 = xs[b][j].pair(i / 2, i % 2 * 2 + 1, p);
+                            mma_16816(sum[b], ones, b0, b1, typename C::Half());
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) mma_16816(d[m][b], a[m], b0, b1, Half());
+                            for (int m = 0; m < MT; ++m) mma_16816(d[m][b], a[m], b0, b1, typename C::Half());
                         }
                 }
                 if (k0 + j >= seg_end) continue;  // behind the last group: zeros so far, and no scale
@@ -253,8 +309,8 @@ __global__ void __launch_bounds__(32 * kW4Warps)
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const ScaleOffset<T> v = table[(k0 + j - seg) * kOut + m * 16 + r * 8 + g];
-                        const float sc = to_f32(v.s), of = fmaf(8.0f, sc, to_f32(v.z));
+                        const ScaleOffset<T> v = table[(k0 + j - seg) * kPitch + m * 16 + r * 8 + g];
+                        const float sc = C::scale(to_f32(v.s)), of = C::offset(to_f32(v.s), to_f32(v.z));
 #pragma unroll
                         for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -266,6 +322,7 @@ __global__ void __launch_bounds__(32 * kW4Warps)
             }
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // the ring becomes the join's memory
     __syncthreads();
     float (*join)[kOut][NT * 8 + 1] = reinterpret_cast<float (*)[kOut][NT * 8 + 1]>(smem);
     // accumulator e of lane (g, t): output g + 8 (e / 2), row 2 t + e % 2

@@ -57,17 +57,6 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
     return v;
 }
 
-// VE elements at a time: one 16-byte access, or single elements where rows do not
-// start on 16-byte boundaries.
-template <typename T, int VE>
-struct alignas(sizeof(T) * VE) Vec {
-    T v[VE];
-};
-template <typename T, int VE>
-__device__ __forceinline__ Vec<T, VE> load(const T* p) {
-    return *reinterpret_cast<const Vec<T, VE>*>(p);
-}
-
 // A row lives in its threads' registers: E elements each, in items of VE, item k of
 // thread t at (k * TPR + t) * VE.  One read of x and the residual, one write of each
 // result.
@@ -87,30 +76,28 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
     for (int k = 0; k < kItems; ++k) {
         const int j = (k * TPR + t) * VE;
         if (live && j < c) {
-            vx[k] = load<T, VE>(x + base + j);
-            if (res) vr[k] = load<T, VE>(res + base + j);
+            vx[k] = load_vec<T, VE>(x + base + j);
+            if (res) vr[k] = load_vec<T, VE>(res + base + j);
         }
     }
     float ss = 0.0f;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int j = (k * TPR + t) * VE;
+        float* hk = h + k * VE;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) h[k * VE + e] = 0.0f;
+        for (int e = 0; e < VE; ++e) hk[e] = 0.0f;
         if (live && j < c) {
+            unpack(vx[k], hk);
+            if (res) {
+                float r[VE];
+                unpack(vr[k], r);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                float v = to_f32(vx[k].v[e]);
-                if (res) v += to_f32(vr[k].v[e]);
-                h[k * VE + e] = v;
-                ss += v * v;
+                for (int e = 0; e < VE; ++e) hk[e] += r[e];
+                if (sum_out) store_vec(sum_out + base + j, pack<T, VE>(hk));
             }
-            if (sum_out) {
-                Vec<T, VE> o;
 #pragma unroll
-                for (int e = 0; e < VE; ++e) o.v[e] = from_f32<T>(h[k * VE + e]);
-                *reinterpret_cast<Vec<T, VE>*>(sum_out + base + j) = o;
-            }
+            for (int e = 0; e < VE; ++e) ss = fmaf(hk[e], hk[e], ss);
         }
     }
     const float rstd = rsqrtf(row_reduce<Sum, TPR>(ss, part[0]) / (float)c + eps);
@@ -119,19 +106,20 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
     for (int k = 0; k < kItems; ++k) {
         const int j = (k * TPR + t) * VE;
         if (!live || j >= c) continue;
-        Vec<T, VE> w;
-        if (weight) w = load<T, VE>(weight + j);
+        float* y = h + k * VE;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            float& y = h[k * VE + e];
-            y = y * rstd * (weight ? to_f32(w.v[e]) : 1.0f);
-            if (Q8) m = max_nan(m, fabsf(y));
+        for (int e = 0; e < VE; ++e) y[e] *= rstd;
+        if (weight) {
+            float w[VE];
+            unpack(load_vec<T, VE>(weight + j), w);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) y[e] *= w[e];
         }
-        if (!Q8) {
-            Vec<T, VE> o;
+        if (Q8) {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) o.v[e] = from_f32<T>(h[k * VE + e]);
-            *reinterpret_cast<Vec<T, VE>*>(out + base + j) = o;
+            for (int e = 0; e < VE; ++e) m = max_nan(m, fabsf(y[e]));
+        } else {
+            store_vec(out + base + j, pack<T, VE>(y));
         }
     }
     if (Q8) {
@@ -238,22 +226,15 @@ __device__ __forceinline__ float group_sum(float v, float* part, int group) {
 constexpr int kAhead = 2, kStages = kAhead + 1;
 template <typename T, int VE, int E>
 constexpr bool kFetchesAhead = VE * sizeof(T) == 16 && E * sizeof(T) <= 32;
-template <typename T, int VE, int TPR, int E>
+template <typename T, int VE, int TPR, int E, bool SUM>
 constexpr int kBackwardSmem =
-    kFetchesAhead<T, VE, E> ? kStages * 3 * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512) : 0;
-
-__device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+    kFetchesAhead<T, VE, E> ? kStages * (SUM ? 3 : 2) * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512) : 0;
 
 // dx of the rows and, in `part`, each CTA's column sums of dy * xh.  A CTA's row groups
 // of TPR threads take rows blockIdx.x * kRows + group, and so on by gridDim.x * kRows,
 // and wait only within the group; a thread keeps the sums of its columns in registers
 // over all its rows, and the groups' sums are joined in shared memory at the end.
-template <typename T, int VE, int TPR, int E>
+template <typename T, int VE, int TPR, int E, bool SUM>
 __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, E == 8 && sizeof(T) == 2 ? 2 : 1)
     k_rms_norm_backward(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
                         const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
@@ -272,78 +253,84 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, E == 8 && sizeof(T) == 
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int j = (k * TPR + t) * VE;
-        if (weight && j < c) w[k] = load<T, VE>(weight + j);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) w[k].v[e] = from_f32<T>(1.0f);
+        if (weight && j < c) w[k] = load_vec<T, VE>(weight + j);
     }
-    const int64_t step = (int64_t)gridDim.x * kRows;
+    const float by_c = 1.0f / (float)c;
+    const int64_t step = (int64_t)gridDim.x * kRows, stride = step * c;
     int64_t i = (int64_t)blockIdx.x * kRows + group;
-    const auto fetch = [&](int64_t row, int stage) {
-        V* to = ring + stage * (3 * kItems * kThreads);
-        if (row < n) {
+    int64_t at = i * c + t * VE, at_fetch = at;  // this thread's first element of a row
+    const auto fetch = [&](bool in, int stage) {
+        V* to = ring + stage * ((SUM ? 3 : 2) * kItems * kThreads);
+        if (in) {
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
-                const int j = (k * TPR + t) * VE;
-                if (j >= c) continue;
-                copy_ahead(to + k * kThreads, dy + row * c + j);
-                copy_ahead(to + (kItems + k) * kThreads, h + row * c + j);
-                if (dsum) copy_ahead(to + (2 * kItems + k) * kThreads, dsum + row * c + j);
+                if ((k * TPR + t) * VE >= c) continue;
+                const int64_t from = at_fetch + k * TPR * VE;
+                copy16_async(to + k * kThreads, dy + from);
+                copy16_async(to + (kItems + k) * kThreads, h + from);
+                if (SUM) copy16_async(to + (2 * kItems + k) * kThreads, dsum + from);
             }
         }
-        copies_group();
+        at_fetch += stride;
+        copy_commit();
     };
     if (kFetch) {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) fetch(i + a * step, a);
+        for (int a = 0; a < kAhead; ++a) fetch(i + a * step < n, a);
     }
     float rstd_next = i < n ? rstd_in[i] : 0.0f;
     int turn = 0;  // the sums' buffer: a thread may still read the last row's
     int stage = 0;
-    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += step, i += step, turn ^= 1) {
+    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += step, i += step, at += stride, turn ^= 1) {
         const bool live = i < n;
         const float rstd = rstd_next;
         rstd_next = i + step < n ? rstd_in[i + step] : 0.0f;
         V vd[kItems], vh[kItems], vs[kItems];
-        const V* from = ring + stage * (3 * kItems * kThreads);
-        if (kFetch) copies_wait();
+        const V* from = ring + stage * ((SUM ? 3 : 2) * kItems * kThreads);
+        if (kFetch) copy_wait<kAhead - 1>();
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int j = (k * TPR + t) * VE;
-            if (live && j < c) {
-                vd[k] = kFetch ? from[k * kThreads] : load<T, VE>(dy + i * c + j);
-                vh[k] = kFetch ? from[(kItems + k) * kThreads] : load<T, VE>(h + i * c + j);
-                if (dsum) vs[k] = kFetch ? from[(2 * kItems + k) * kThreads] : load<T, VE>(dsum + i * c + j);
-            }
+            if (!live || (k * TPR + t) * VE >= c) continue;
+            vd[k] = kFetch ? from[k * kThreads] : load_vec<T, VE>(dy + at + k * TPR * VE);
+            vh[k] = kFetch ? from[(kItems + k) * kThreads] : load_vec<T, VE>(h + at + k * TPR * VE);
+            if (SUM) vs[k] = kFetch ? from[(2 * kItems + k) * kThreads] : load_vec<T, VE>(dsum + at + k * TPR * VE);
         }
         float g[E], xh[E], dot = 0.0f;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             if (!live || (k * TPR + t) * VE >= c) continue;
+            float d[VE], wk[VE];
+            unpack(vd[k], d);
+            unpack(vh[k], xh + k * VE);
+            unpack(w[k], wk);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const int at = k * VE + e;
-                const float d = to_f32(vd[k].v[e]);
-                xh[at] = to_f32(vh[k].v[e]) * rstd;
-                g[at] = weight ? d * to_f32(w[k].v[e]) : d;
-                dw[at] = fmaf(d, xh[at], dw[at]);
-                dot = fmaf(g[at], xh[at], dot);
+                const int o = k * VE + e;
+                xh[o] *= rstd;
+                g[o] = d[e] * wk[e];
+                dw[o] = fmaf(d[e], xh[o], dw[o]);
+                dot = fmaf(g[o], xh[o], dot);
             }
         }
         if (kFetch) {
             // into the stage read in the last turn
-            fetch(i + kAhead * step, stage == 0 ? kStages - 1 : stage - 1);
+            fetch(i + kAhead * step < n, stage == 0 ? kStages - 1 : stage - 1);
             stage = stage == kStages - 1 ? 0 : stage + 1;
         }
-        const float mean = group_sum<TPR>(dot, red[turn], group) / (float)c;
+        const float mean = group_sum<TPR>(dot, red[turn], group) * by_c;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int j = (k * TPR + t) * VE;
-            if (!live || j >= c) continue;
-            V o;
+            if (!live || (k * TPR + t) * VE >= c) continue;
+            float o[VE], ds[VE];
+            if (SUM) unpack(vs[k], ds);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const int at = k * VE + e;
-                o.v[e] = from_f32<T>(fmaf(rstd, fmaf(-xh[at], mean, g[at]), dsum ? to_f32(vs[k].v[e]) : 0.0f));
+                o[e] = fmaf(-xh[k * VE + e], mean, g[k * VE + e]);
+                o[e] = SUM ? fmaf(rstd, o[e], ds[e]) : rstd * o[e];
             }
-            *reinterpret_cast<V*>(dx + i * c + j) = o;
+            store_vec(dx + at + k * TPR * VE, pack<T, VE>(o));
         }
     }
     if (!part) return;
@@ -470,18 +457,22 @@ void launch_forward_as(const NormArgs& a) {
         static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
 }
 
-// Returns the CTAs that wrote column sums.
-template <typename T, int VE, int TPR, int E>
-int launch_backward_as(const NormArgs& a) {
-    constexpr int kThreads = TPR > 512 ? TPR : 512;
-    constexpr int kSmem = kBackwardSmem<T, VE, TPR, E>;
+template <typename T, int VE, int TPR, int E, bool SUM>
+int launch_backward_sum(const NormArgs& a) {
+    constexpr int kThreads = TPR > 512 ? TPR : 512, kSmem = kBackwardSmem<T, VE, TPR, E, SUM>;
     const int parts = row_parts(a.n, kThreads / TPR);
     if (kSmem > 48 * 1024 - 16640)  // with the static arrays over what a launch has without asking
-        cudaFuncSetAttribute(k_rms_norm_backward<T, VE, TPR, E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    k_rms_norm_backward<T, VE, TPR, E><<<parts, kThreads, kSmem, a.stream>>>(
+        cudaFuncSetAttribute(k_rms_norm_backward<T, VE, TPR, E, SUM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    k_rms_norm_backward<T, VE, TPR, E, SUM><<<parts, kThreads, kSmem, a.stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
         static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
     return parts;
+}
+
+// Returns the CTAs that wrote column sums.
+template <typename T, int VE, int TPR, int E>
+int launch_backward_as(const NormArgs& a) {
+    return a.dsum ? launch_backward_sum<T, VE, TPR, E, true>(a) : launch_backward_sum<T, VE, TPR, E, false>(a);
 }
 
 // A thread holds up to 32 elements of a row; the fewest threads that hold it take it.

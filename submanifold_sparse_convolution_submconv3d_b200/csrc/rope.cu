@@ -36,13 +36,16 @@ struct RopeArgs {
     float sign;         // -1: turn back
 };
 
-// An item's elements: one 16-byte access, or single elements at any address.
-template <typename T, int VE>
-struct alignas(sizeof(T) * VE == 16 ? 16 : sizeof(T)) Vec {
-    T v[VE];
-};
-
 constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 2;  // voxels a lane fetches ahead, through shared memory
+
+template <typename T, int VE>
+constexpr bool kWide = sizeof(T) * VE == 16;
+// Heads a lane turns of a voxel, one after the other: 64 bytes on the way a voxel.
+template <bool HALVES>
+constexpr int kPasses = HALVES ? 2 : 4;
+template <typename T, int VE>
+constexpr int kRopeSmem = kWide<T, VE> ? (kRopeAhead + 1) * 4 * 16 * kRopeThreads : 0;
 
 // Items: VE neighbouring elements of a head (VE / 2 pairs) in the interleaved layout,
 // VE elements of either half (VE pairs) in the halves layout.
@@ -50,15 +53,19 @@ constexpr int kRopeThreads = 256;
 // A lane owns one item position of the head for the whole launch, so the cosines and
 // sines of its pairs are computed once a voxel and used for all of the voxel's heads
 // that the warp turns: head_slots heads (and, where a voxel has few heads, voxel_slots
-// voxels) side by side, kInFlight of them one after the other with their loads issued
-// before the sines.  Warps go from voxel to voxel, the next coordinates loaded ahead.
-// blockIdx.y: the block of items and the group of heads.
+// voxels) side by side, kPasses of them one after the other.  Warps go from voxel to
+// voxel with the next coordinates in registers and the items of the next two voxels on
+// their way into shared memory; every lane copies and reads its own, so none waits for
+// another.  blockIdx.y: the block of items and the group of heads.
 template <typename T, int VE, bool HALVES>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
     k_rope(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a, const T* x, T* out) {
     constexpr int kPairs = HALVES ? VE : VE / 2;  // pairs an item
-    constexpr int kInFlight = HALVES ? 2 : 4;
+    constexpr int kVecs = HALVES ? 2 : 1;         // accesses an item
+    constexpr int kN = kPasses<HALVES>;
+    constexpr bool kRing = kWide<T, VE>;
     using V = Vec<T, VE>;
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint64_t turn[kMaxPairs];
     for (int j = threadIdx.x; j < a.pairs; j += kRopeThreads) turn[j] = tab.turn[j];
     __syncthreads();
@@ -66,65 +73,84 @@ __global__ void __launch_bounds__(kRopeThreads)
     const int hg = (int)blockIdx.y / a.chunk_blocks, cb = (int)blockIdx.y - hg * a.chunk_blocks;
     const int slot = lane / a.lanes_head, chunk = cb * 32 + lane % a.lanes_head;
     const int vs = slot / a.head_slots;
-    const bool active = vs < a.voxel_slots && chunk < a.chunks;
-    if (!active) return;
+    if (vs >= a.voxel_slots || chunk >= a.chunks) return;
     const int h0 = hg * a.unit_heads + slot % a.head_slots, h_end = min(a.heads, (hg + 1) * a.unit_heads);
     const int j0 = chunk * kPairs;
+    const int64_t i0 = ((int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)) * a.voxel_slots + vs;
+    if (i0 >= a.n || h0 >= h_end) return;
+    const int todo = (h_end - h0 + a.head_slots - 1) / a.head_slots;  // passes of this lane, at most kN
     uint32_t axes = 0;  // two bits a pair: 0 does not turn, else the axis + 1
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) axes |= (uint32_t)(tab.axis[j0 + p] + 1) << (2 * p);
     const int64_t step = (int64_t)gridDim.x * (kRopeThreads / 32) * a.voxel_slots;
-    int64_t i = ((int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5)) * a.voxel_slots + vs;
-    const int64_t x_step = a.head_slots * a.x_head, o_step = a.head_slots * a.o_head;
-    int4 at = i < a.n ? a.coords[i] : make_int4(0, 0, 0, 0);
-    for (; i < a.n; i += step) {
+    const int64_t x_pass = a.head_slots * a.x_head, o_pass = a.head_slots * a.o_head;
+    const int64_t x_step = step * a.x_row, o_step = step * a.o_row;
+    const T* px = x + i0 * a.x_row + h0 * a.x_head + chunk * VE;
+    T* po = out + i0 * a.o_row + h0 * a.o_head + chunk * VE;
+    V* ring = reinterpret_cast<V*>(smem) + threadIdx.x;  // [stage][pass, half][thread]
+    const auto fetch = [&](bool in, int stage) {
+        if (in) {
+#pragma unroll
+            for (int k = 0; k < kN; ++k) {
+                if (k >= todo) continue;
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+                    copy16_async(ring + ((stage * kN + k) * kVecs + v) * kRopeThreads, px + k * x_pass + v * a.pairs);
+            }
+        }
+        px += x_step;
+        copy_commit();
+    };
+    if (kRing) {
+#pragma unroll
+        for (int s = 0; s < kRopeAhead; ++s) fetch(i0 + s * step < a.n, s);
+    }
+    int4 at = a.coords[i0];
+    int stage = 0;
+    for (int64_t i = i0; i < a.n; i += step) {
+        if (kRing) fetch(i + kRopeAhead * step < a.n, stage == 0 ? kRopeAhead : stage - 1);  // read in the last turn
         const int4 pos = at;
         if (i + step < a.n) at = a.coords[i + step];
-        const T* px = x + i * a.x_row + h0 * a.x_head + chunk * VE;
-        T* po = out + i * a.o_row + h0 * a.o_head + chunk * VE;
         float cs[kPairs], sn[kPairs];
-        for (int h = h0; h < h_end; h += kInFlight * a.head_slots) {
-            V lo[kInFlight], hi[HALVES ? kInFlight : 1];
 #pragma unroll
-            for (int k = 0; k < kInFlight; ++k) {
-                if (h + k * a.head_slots >= h_end) continue;
-                lo[k] = *reinterpret_cast<const V*>(px + k * x_step);
-                if (HALVES) hi[HALVES ? k : 0] = *reinterpret_cast<const V*>(px + k * x_step + a.pairs);
+        for (int p = 0; p < kPairs; ++p) {
+            const uint32_t ax = (axes >> (2 * p)) & 3u;
+            const int c = ax == 1 ? pos.y : ax == 2 ? pos.z : ax == 3 ? pos.w : 0;
+            const int32_t frac = (int32_t)((turn[j0 + p] * (uint64_t)(int64_t)c) >> 32);
+            if (sizeof(T) == 2) {
+                // 2^-21.2 of error on [-pi, pi], against the 2^-9 of the result's rounding
+                const float ang = (float)frac * 1.46291807926715968e-9f;  // 2 pi / 2^32
+                sn[p] = __sinf(ang) * a.sign;
+                cs[p] = __cosf(ang);
+            } else {
+                sincospif((float)frac * 0x1p-31f, &sn[p], &cs[p]);
+                sn[p] *= a.sign;
             }
-            px += kInFlight * x_step;
-            if (h == h0) {
-#pragma unroll
-                for (int p = 0; p < kPairs; ++p) {
-                    const uint32_t ax = (axes >> (2 * p)) & 3u;
-                    const int c = ax == 1 ? pos.y : ax == 2 ? pos.z : ax == 3 ? pos.w : 0;
-                    const int32_t frac = (int32_t)((turn[j0 + p] * (uint64_t)(int64_t)c) >> 32);
-                    if (sizeof(T) == 2) {
-                        // 2^-21.2 of error on [-pi, pi], against the 2^-9 of the result's rounding
-                        const float ang = (float)frac * 1.46291807926715968e-9f;  // 2 pi / 2^32
-                        sn[p] = __sinf(ang) * a.sign;
-                        cs[p] = __cosf(ang);
-                    } else {
-                        sincospif((float)frac * 0x1p-31f, &sn[p], &cs[p]);
-                        sn[p] *= a.sign;
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kInFlight; ++k) {
-                if (h + k * a.head_slots >= h_end) continue;
-#pragma unroll
-                for (int p = 0; p < kPairs; ++p) {
-                    T& ra = HALVES ? lo[k].v[p] : lo[k].v[2 * p];
-                    T& rb = HALVES ? hi[HALVES ? k : 0].v[p] : lo[k].v[HALVES ? 0 : 2 * p + 1];
-                    const float u = to_f32(ra), v = to_f32(rb);
-                    ra = from_f32<T>(u * cs[p] - v * sn[p]);
-                    rb = from_f32<T>(u * sn[p] + v * cs[p]);
-                }
-                *reinterpret_cast<V*>(po + k * o_step) = lo[k];
-                if (HALVES) *reinterpret_cast<V*>(po + k * o_step + a.pairs) = hi[HALVES ? k : 0];
-            }
-            po += kInFlight * o_step;
         }
+        if (kRing) copy_wait<kRopeAhead>();
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            if (k >= todo) continue;
+            float f[kVecs * VE];
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                unpack(kRing ? ring[((stage * kN + k) * kVecs + v) * kRopeThreads]
+                             : load_vec<T, VE>(px + k * x_pass + v * a.pairs),
+                       f + v * VE);
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+                float& u = HALVES ? f[p] : f[2 * p];
+                float& v = HALVES ? f[(kVecs - 1) * VE + p] : f[2 * p + 1 - (HALVES ? 1 : 0)];
+                const float turned = u * cs[p] - v * sn[p];
+                v = u * sn[p] + v * cs[p];
+                u = turned;
+            }
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) store_vec(po + k * o_pass + v * a.pairs, pack<T, VE>(f + v * VE));
+        }
+        if (!kRing) px += x_step;
+        po += o_step;
+        stage = stage == kRopeAhead ? 0 : stage + 1;
     }
 }
 
@@ -137,7 +163,7 @@ int device_sms() {
 
 template <typename T, int VE, bool HALVES>
 void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cudaStream_t st) {
-    constexpr int kInFlight = HALVES ? 2 : 4, kWarps = kRopeThreads / 32;
+    constexpr int kN = kPasses<HALVES>, kWarps = kRopeThreads / 32, kSmem = kRopeSmem<T, VE>;
     const int sms = device_sms();
     a.chunks = a.pairs / (HALVES ? VE : VE / 2);
     a.chunk_blocks = (a.chunks + 31) / 32;
@@ -145,17 +171,20 @@ void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cud
     const int slots = 32 / a.lanes_head;
     a.head_slots = slots < a.heads ? slots : a.heads;
     a.voxel_slots = slots / a.head_slots;
-    // Heads a warp: as many as it has in flight, so that a voxel's coordinates and sines
-    // are used often; where that leaves warps without work, one load a lane.
+    // Heads a warp: kPasses a lane, so that a voxel's coordinates and sines are used
+    // often, dealt evenly; where that leaves warps without work, one.
     const int64_t warps = (a.n + a.voxel_slots - 1) / a.voxel_slots * a.chunk_blocks;
     const int passes = (a.heads + a.head_slots - 1) / a.head_slots;
-    int per = passes <= 2 * kInFlight ? passes : kInFlight;
-    if (warps * ((passes + per - 1) / per) < (int64_t)sms * 2 * kWarps) per = 1;
+    int groups = (passes + kN - 1) / kN;
+    if (warps * groups < (int64_t)sms * 2 * kWarps || groups * a.chunk_blocks > 65535) groups = passes;
+    const int per = (passes + groups - 1) / groups;
     a.unit_heads = per * a.head_slots;
-    const int groups = (passes + per - 1) / per;  // at most 65535: heads are
+    groups = (passes + per - 1) / per;
     const int64_t blocks = (a.n + (int64_t)a.voxel_slots * kWarps - 1) / ((int64_t)a.voxel_slots * kWarps);
-    const int64_t most = ((int64_t)sms * 8 + groups * a.chunk_blocks - 1) / (groups * a.chunk_blocks);
-    k_rope<T, VE, HALVES><<<dim3((unsigned)(blocks < most ? blocks : most), groups * a.chunk_blocks), kRopeThreads, 0,
+    const int64_t most = ((int64_t)sms * 4 + groups * a.chunk_blocks - 1) / (groups * a.chunk_blocks);
+    if (kSmem + (int)sizeof(uint64_t) * kMaxPairs > 48 * 1024)
+        cudaFuncSetAttribute(k_rope<T, VE, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    k_rope<T, VE, HALVES><<<dim3((unsigned)(blocks < most ? blocks : most), groups * a.chunk_blocks), kRopeThreads, kSmem,
                             st>>>(tab, a, static_cast<const T*>(x), static_cast<T*>(out));
 }
 

@@ -49,6 +49,63 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// VE elements at a time: one 16-byte access, or single elements at any address.
+template <typename T, int VE>
+struct alignas(sizeof(T) * VE == 16 ? 16 : sizeof(T)) Vec {
+    T v[VE];
+};
+template <typename T, int VE>
+__device__ __forceinline__ Vec<T, VE> load_vec(const T* p) {
+    return *reinterpret_cast<const Vec<T, VE>*>(p);
+}
+template <typename T, int VE>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, VE>& v) {
+    *reinterpret_cast<Vec<T, VE>*>(p) = v;
+}
+
+// The elements as fp32 and back, bf16 two at a time.
+template <typename T, int VE>
+__device__ __forceinline__ void unpack(const Vec<T, VE>& v, float* f) {
+    if constexpr (sizeof(T) == 2 && VE % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VE; e += 2) {
+            const uint32_t two = (uint32_t)__bfloat16_as_ushort(v.v[e]) | ((uint32_t)__bfloat16_as_ushort(v.v[e + 1]) << 16);
+            f[e] = __uint_as_float(two << 16);
+            f[e + 1] = __uint_as_float(two & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = to_f32(v.v[e]);
+    }
+}
+template <typename T, int VE>
+__device__ __forceinline__ Vec<T, VE> pack(const float* f) {
+    Vec<T, VE> v;
+    if constexpr (sizeof(T) == 2 && VE % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < VE; e += 2) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(f[e], f[e + 1]);
+            v.v[e] = two.x;
+            v.v[e + 1] = two.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) v.v[e] = from_f32<T>(f[e]);
+    }
+    return v;
+}
+
+// 16 bytes from global to shared memory, asynchronously; groups complete in order.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // max that keeps a NaN of either side (fmaxf drops it)
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
