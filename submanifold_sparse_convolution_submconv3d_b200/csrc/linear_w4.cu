@@ -135,30 +135,25 @@ struct XShare<float, W> {
     }
 };
 
-constexpr int kW4Warps = 8;
-constexpr int kW4Chunk = 128;  // input channels a warp takes at a time: 16 codes words a row
-
-constexpr int kW4Segment = 64;  // groups whose scales a CTA holds in shared memory
-
-// A scale and its offset side by side, read with one access.
-template <typename T>
-struct alignas(2 * sizeof(T)) ScaleOffset {
-    T s, z;
+// A launch's shape.  NT: blocks of 8 rows a CTA holds; then, of the 65,536 registers of
+// an SM, KC input channels of x, 16 MT outputs' sums and the next channels of x fit
+// WARPS warps (fp32 rows take three parts each).
+template <typename X, int NT>
+struct W4Shape {
+    static constexpr int kChunk = NT == 4 || sizeof(X) == 4 ? 64 : 128;
+    static constexpr int kTiles = NT == 4 || sizeof(X) == 4 ? 4 : 8;
+    static constexpr int kWarps = NT == 1 && sizeof(X) < 4 ? 16 : 12;
+    static constexpr int kThreads = 32 * kWarps;
+    // steps (a tile of a chunk) of codes on the way: a power of two of them in the ring
+    static constexpr int kRing = 8, kAhead = kRing - 1;
+    static constexpr int kStepBytes = 2 * (kChunk / 8) * kThreads;  // of codes, over all warps
+    static constexpr int kRingBytes = kRing * kStepBytes;
 };
+constexpr int kW4TableBytes = 72 * 1024;  // scales and offsets held at a time, at most
 
-// Chunks of codes a warp has on the way besides the one it works on, through shared
-// memory (each thread copies its own words).
-template <int MT>
-constexpr int kW4Ahead = MT == 4 ? 1 : MT == 2 ? 2 : 3;
-
-template <int MT>
-constexpr int kW4Ring = (kW4Ahead<MT> + 1) * MT * 2 * 16 * 32 * kW4Warps;
-template <typename T, int MT, int NT>
-inline int w4_smem(int groups) {
-    const int table = (groups < kW4Segment ? groups : kW4Segment) * (MT * 16 + 1) * (int)sizeof(ScaleOffset<T>);
-    const int join = kW4Warps * MT * 16 * (NT * 8 + 1) * 4, work = kW4Ring<MT> + table;
-    return work > join ? work : join;
-}
+// Bytes between two outputs' scales in shared memory: 16 more than a multiple of 32, so
+// that eight outputs' reads fall on different banks.
+inline int w4_pitch(int groups, int elem) { return (groups * elem + 31) / 32 * 32 + 16; }
 
 template <int BYTES>
 __device__ __forceinline__ void copy_words(void* dst, const void* src, bool in) {
@@ -171,177 +166,219 @@ __device__ __forceinline__ void copy_words(void* dst, const void* src, bool in) 
                      : "memory");
 }
 
-// A CTA multiplies 16 MT outputs by 8 NT rows; a warp takes every kW4Warps-th chunk of
-// the input channels, and the warps' sums are joined in shared memory.
+struct W4Params {
+    const float* x_scale;
+    int n, cin, cout;
+    int tiles;        // tiles of 16 outputs a CTA
+    int seg_groups;   // groups whose scales a CTA holds at a time
+    int pitch;        // bytes between two outputs' scales in shared memory
+};
+
+// A CTA multiplies `tiles` tiles of 16 outputs by 8 NT rows.  A warp takes every
+// kWarps-th chunk of the input channels: it holds the chunk's part of x in registers, as
+// the tensor-core operand, and streams the tiles' codes past it; the warps' sums are
+// joined in shared memory at the end.  What bounds it: the codes' way from memory (for
+// more than 16 rows the tensor cores), so the codes of the next seven steps are on
+// their way into shared memory (each thread copies and reads its own words, so no warp
+// waits for another) and the next chunk's x into registers.
 //
 // Fragments.  In one 16 x 8 x 16 step lane (g, t) = (lane / 4, lane % 4) holds four
 // input channels of outputs g and g + 8 and of row g; which four is free as long as both
-// operands agree.  A group's scale must be common to the step, so lane t owns the
-// group's words [t W, t W + W), W = GROUP / 32, neighbouring in memory: W words of
-// either output with one load, and each word gives two steps.
+// operands agree.  A group's scale must be common to the step, so of a part of SUB
+// channels (a group, or as much of it as a chunk has) lane t owns the words
+// [t W, t W + W), W = SUB / 32, neighbouring in memory, and each word gives two steps.
 //
-// Scales.  Over a group the sum of f(q) x is the step's accumulator, started at zero
-// for each group; the sum of x comes out of the same instruction with ones in place of
-// the codes.  The scales of the CTA's outputs are brought into shared memory along the
+// Scales.  Over a part the sum of f(q) x is the step's accumulator, started at zero for
+// each part; the sum of x comes out of the same instruction with ones in place of the
+// codes, once for all tiles.  The CTA's scales are brought into shared memory along the
 // groups, as they lie in memory; read per lane from global memory, each of them would
 // cost a cache line's lookup.
-template <typename T, typename X, int MT, int NT, int GROUP>
-__global__ void __launch_bounds__(32 * kW4Warps)
-    k_linear_w4(const X* __restrict__ x, const float* __restrict__ x_scale, int n, int cin,
-                const uint32_t* __restrict__ packed, const T* __restrict__ scales, const T* __restrict__ offsets,
-                const T* __restrict__ bias, T* __restrict__ out, int cout) {
-    constexpr int kW = GROUP / 32, kGroups = kW4Chunk / GROUP, kOut = MT * 16, kThreads = 32 * kW4Warps;
-    constexpr int kAhead = kW4Ahead<MT>, kPitch = kOut + 1;
-    using Share = XShare<X, kW>;
+template <typename T, typename X, int NT, int GROUP>
+__global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
+    k_linear_w4(const X* __restrict__ x, const uint32_t* __restrict__ packed, const T* __restrict__ scales,
+                const T* __restrict__ offsets, const T* __restrict__ bias, T* __restrict__ out, const W4Params a) {
+    using S = W4Shape<X, NT>;
     using C = Codes<X>;
-    constexpr int kParts = Share::kParts;
+    constexpr int kChunk = S::kChunk, kSub = GROUP < kChunk ? GROUP : kChunk, kW = kSub / 32, kSubs = kChunk / kSub;
+    constexpr int kLane = kChunk / 32;  // words a lane has of an output's chunk
+    using Share = XShare<X, kW>;
+    constexpr int kParts = Share::kParts, kMt = S::kTiles, kThreads = S::kThreads, kWarps = S::kWarps;
     extern __shared__ __align__(16) unsigned char smem[];
-    // [stage][output tile and half][4 words a lane][thread]
-    uint32_t* ring = reinterpret_cast<uint32_t*>(smem);
-    ScaleOffset<T>* table = reinterpret_cast<ScaleOffset<T>*>(smem + kW4Ring<MT>);  // [group of the segment][output]
+    uint32_t* ring = reinterpret_cast<uint32_t*>(smem) + threadIdx.x * kLane;  // [step][output half][thread][word]
+    unsigned char* table = smem + S::kRingBytes;                              // [scale, offset][output][group]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int o0 = blockIdx.x * kOut, row0 = blockIdx.y * NT * 8;
-    const int words = cin / 8, groups = cin / GROUP;
-    float y[MT][NT][4];
+    const int words = a.cin / 8, groups = a.cin / GROUP, chunks = (a.cin + kChunk - 1) / kChunk;
+    const int o0 = blockIdx.x * a.tiles * 16, row0 = blockIdx.y * NT * 8;
+    const int tiles = min(a.tiles, (a.cout - o0 + 15) / 16);
+    float y[kMt][NT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < kMt; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[m][b][e] = 0.0f;
 
-    // The words of a chunk's group j are copied together; a stage holds, per output, the
-    // groups' words one after the other: word j kW + i of the lane.
-    const uint32_t* mine = packed + (int64_t)(o0 + g) * words + t * kW;
-    const auto fetch = [&](int k0, int stage) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
+    // The codes' way: step after step, tile after tile of a chunk, then the next chunk.
+    int f_tile = 0, f_chunk = warp, f_slot = 0;
+    const auto fetch = [&]() {
+        if (f_chunk < chunks) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                uint32_t* to = ring + ((stage * MT * 2 + m * 2 + r) * kThreads + threadIdx.x) * 4;
-                const bool row_in = o0 + m * 16 + r * 8 + g < cout;
+                const int o = o0 + f_tile * 16 + r * 8 + g;
+                uint32_t* to = ring + (f_slot * 2 + r) * (kThreads * kLane);
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const bool in = row_in && k0 + j < groups;
-                    copy_words<4 * kW>(to + j * kW, in ? mine + (m * 16 + r * 8) * (int64_t)words + (k0 + j) * (GROUP / 8) : packed,
-                                       in);
+                for (int j = 0; j < kSubs; ++j) {
+                    const int word = f_chunk * (kChunk / 8) + j * (kSub / 8) + t * kW;
+                    const bool in = o < a.cout && word < words;
+                    copy_words<4 * kW>(to + j * kW, in ? packed + (int64_t)o * words + word : packed, in);
                 }
             }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++f_tile == tiles) {
+                f_tile = 0;
+                f_chunk += kWarps;
+            }
+        }
+        f_slot = (f_slot + 1) % S::kRing;
+        copy_commit();
     };
-    constexpr int kStep = kW4Warps * kGroups;
-    int k0 = warp * kGroups, stage = 0;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) fetch(k0 + a * kStep, a);
-    for (int seg = 0; seg < groups; seg += kW4Segment) {
-        const int seg_end = min(groups, seg + kW4Segment);
+    for (int s = 0; s < S::kAhead; ++s) fetch();
+    const auto load_x = [&](Share (&xs)[NT][kSubs], int chunk) {
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int j = 0; j < kSubs; ++j) {
+                const int row = row0 + b * 8 + g, k = chunk * kChunk + j * kSub + t * kW * 8;
+                xs[b][j].load(x + (int64_t)row * a.cin + k, row < a.n && k < a.cin);
+            }
+    };
+    Share raw[NT][kSubs];
+    load_x(raw, warp);
+
+    int slot = 0, chunk = warp;
+    for (int seg = 0; seg < groups; seg += a.seg_groups) {
+        const int held = min(a.seg_groups, groups - seg), rows = min(tiles * 16, a.cout - o0);
         if (seg) __syncthreads();
-        for (int o = warp; o < kOut; o += kW4Warps)
-            for (int k = seg + lane; k < seg_end; k += 32) {
-                ScaleOffset<T> v;
-                v.s = v.z = from_f32<T>(0.0f);
-                if (o0 + o < cout) {
-                    v.s = scales[(int64_t)(o0 + o) * groups + k];
-                    v.z = offsets[(int64_t)(o0 + o) * groups + k];
-                }
-                table[(k - seg) * kPitch + o] = v;
+        for (int z = 0; z < 2; ++z) {
+            const T* from = (z ? offsets : scales) + (int64_t)o0 * groups + seg;
+            unsigned char* to = table + z * (a.tiles * 16) * a.pitch;
+            constexpr int kVe = 16 / (int)sizeof(T);
+            if (groups % kVe == 0 && seg % kVe == 0) {
+                const int vecs = (held + kVe - 1) / kVe, per = kThreads / 32;
+                for (int o = warp; o < rows; o += per)
+                    for (int v = lane; v < vecs; v += 32)
+                        *reinterpret_cast<uint4*>(to + o * a.pitch + v * 16) =
+                            *reinterpret_cast<const uint4*>(from + (int64_t)o * groups + v * kVe);
+            } else {
+                for (int o = warp; o < rows; o += kThreads / 32)
+                    for (int v = lane; v < held; v += 32)
+                        *reinterpret_cast<T*>(to + o * a.pitch + v * (int)sizeof(T)) = from[(int64_t)o * groups + v];
             }
+        }
         __syncthreads();
-        for (; k0 < seg_end; k0 += kStep) {
-            fetch(k0 + kAhead * kStep, stage == 0 ? kAhead : stage - 1);  // the stage read in the last turn
-            Share xs[NT][kGroups];
-            if (NT == 1) {
+        for (; chunk < chunks && chunk * kChunk < (seg + held) * GROUP; chunk += kWarps) {
+            uint32_t pairs[NT][kSubs][kW][4][kParts];
+            float sum[NT][kSubs][4];
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j)
-                    xs[0][j].load(x + (int64_t)(row0 + g) * cin + (k0 + j) * GROUP + t * kW * 8,
-                                  row0 + g < n && k0 + j < groups);
-            }
-            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-            uint4 w[MT][2];
+            for (int b = 0; b < NT; ++b)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int j = 0; j < kSubs; ++j) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    w[m][r] = *reinterpret_cast<const uint4*>(
-                        ring + ((stage * MT * 2 + m * 2 + r) * kThreads + threadIdx.x) * 4);
-            stage = stage == kAhead ? 0 : stage + 1;
-            const auto word = [](const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
-#pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                if (NT > 1) {
-#pragma unroll
-                    for (int b = 0; b < NT; ++b) {
-                        const int row = row0 + b * 8 + g;
-                        xs[b][j].load(x + (int64_t)row * cin + (k0 + j) * GROUP + t * kW * 8, row < n && k0 + j < groups);
-                    }
-                }
-                float d[MT][NT][4], sum[NT][4];
-#pragma unroll
-                for (int b = 0; b < NT; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sum[b][e] = 0.0f;
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) d[m][b][e] = 0.0f;
-                    }
-#pragma unroll
-                for (int i = 0; i < 2 * kW; ++i) {
-                    uint32_t a[MT][4];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            a[m][e] = C::pair(word(w[m][e & 1], j * kW + i / 2), i % 2 * 2 + (e >> 1));
+                    for (int e = 0; e < 4; ++e) sum[b][j][e] = 0.0f;
                     const uint32_t ones[4] = {C::kOne[0], C::kOne[0], C::kOne[1], C::kOne[1]};
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p)
+                    for (int i = 0; i < kW; ++i)
 #pragma unroll
-                        for (int b = 0; b < NT; ++b) {
-                            const uint32_t b0 = xs[b][j].pair(i / 2, i % 2 * 2, p);
-                            const uint32_t b1 = xs[b][j].pair(i / 2, i % 2 * 2 + 1, p);
-                            mma_16816(sum[b], ones, b0, b1, typename C::Half());
+                        for (int p = 0; p < kParts; ++p) {
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) mma_16816(d[m][b], a[m], b0, b1, typename C::Half());
+                            for (int e = 0; e < 4; ++e) pairs[b][j][i][e][p] = raw[b][j].pair(i, e, p);
+                            mma_16816(sum[b][j], ones, pairs[b][j][i][0][p], pairs[b][j][i][1][p], typename C::Half());
+                            mma_16816(sum[b][j], ones, pairs[b][j][i][2][p], pairs[b][j][i][3][p], typename C::Half());
                         }
                 }
-                if (k0 + j >= seg_end) continue;  // behind the last group: zeros so far, and no scale
+            if (chunk + kWarps < chunks) load_x(raw, chunk + kWarps);
+            const int at = chunk * kChunk / GROUP - seg;  // the chunk's first group in the table
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < kMt; ++m) {
+                if (m >= tiles) continue;
+                fetch();  // into the slot read in the last step
+                copy_wait<S::kAhead>();
+                uint32_t w[2][kLane];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t* from = ring + (slot * 2 + r) * (kThreads * kLane);
+                    if (kLane == 4) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(from);
+                        w[r][0] = v.x, w[r][1] = v.y, w[r][2 % kLane] = v.z, w[r][3 % kLane] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(from);
+                        w[r][0] = v.x, w[r][1] = v.y;
+                    }
+                }
+                slot = (slot + 1) % S::kRing;
+#pragma unroll
+                for (int j = 0; j < kSubs; ++j) {
+                    float d[NT][4];
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[b][e] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 2 * kW; ++i) {
+                        const uint32_t code[4] = {C::pair(w[0][j * kW + i / 2], i % 2 * 2), C::pair(w[1][j * kW + i / 2], i % 2 * 2),
+                                                  C::pair(w[0][j * kW + i / 2], i % 2 * 2 + 1),
+                                                  C::pair(w[1][j * kW + i / 2], i % 2 * 2 + 1)};
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+                                mma_16816(d[b], code, pairs[b][j][i / 2][i % 2 * 2][p], pairs[b][j][i / 2][i % 2 * 2 + 1][p],
+                                          typename C::Half());
+                    }
+                    // (behind the last group of the last chunk: sums of zero and the pitch's rest)
+                    const int k = min(at + j, held - 1);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const ScaleOffset<T> v = table[(k0 + j - seg) * kPitch + m * 16 + r * 8 + g];
-                        const float sc = C::scale(to_f32(v.s)), of = C::offset(to_f32(v.s), to_f32(v.z));
+                        const unsigned char* p = table + (m * 16 + r * 8 + g) * a.pitch + k * (int)sizeof(T);
+                        const float s = to_f32(*reinterpret_cast<const T*>(p));
+                        const float z = to_f32(*reinterpret_cast<const T*>(p + a.tiles * 16 * a.pitch));
+                        const float sc = C::scale(s), of = C::offset(s, z);
 #pragma unroll
                         for (int b = 0; b < NT; ++b)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 float& to = y[m][b][2 * r + e];
-                                to = fmaf(sc, d[m][b][2 * r + e], fmaf(of, sum[b][e], to));
+                                to = fmaf(sc, d[b][2 * r + e], fmaf(of, sum[b][j][e], to));
                             }
                     }
+                }
             }
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");  // the ring becomes the join's memory
+    copy_wait<0>();  // the ring becomes the join's memory
     __syncthreads();
-    float (*join)[kOut][NT * 8 + 1] = reinterpret_cast<float (*)[kOut][NT * 8 + 1]>(smem);
+    float (*join)[kMt * 16][NT * 8 + 1] = reinterpret_cast<float (*)[kMt * 16][NT * 8 + 1]>(smem);
     // accumulator e of lane (g, t): output g + 8 (e / 2), row 2 t + e % 2
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < kMt; ++m) {
+        if (m >= tiles) continue;
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) join[warp][m * 16 + (e >> 1) * 8 + g][b * 8 + 2 * t + (e & 1)] = y[m][b][e];
+    }
     __syncthreads();
-    for (int at = threadIdx.x; at < kOut * NT * 8; at += kThreads) {
-        const int o = at % kOut, r = at / kOut;
-        if (o0 + o >= cout || row0 + r >= n) continue;
-        float v = 0.0f;
+    const int outs = tiles * 16;
+    for (int r = warp; r < NT * 8 && row0 + r < a.n; r += kWarps) {
+        const float xs = a.x_scale ? a.x_scale[row0 + r] : 1.0f;
+        for (int o = lane; o < outs && o0 + o < a.cout; o += 32) {
+            float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kW4Warps; ++k) v += join[k][o][r];
-        if (x_scale) v *= x_scale[row0 + r];
-        if (bias) v += to_f32(bias[o0 + o]);
-        out[(int64_t)(row0 + r) * cout + o0 + o] = from_f32<T>(v);
+            for (int k = 0; k < kWarps; ++k) v += join[k][o][r];
+            v *= xs;
+            if (bias) v += to_f32(bias[o0 + o]);
+            out[(int64_t)(row0 + r) * a.cout + o0 + o] = from_f32<T>(v);
+        }
     }
 }
 
@@ -413,50 +450,47 @@ spconv_status_t w4_args(spconv_dtype_t dtype, const void* packed, const void* sc
 }
 
 struct W4Args {
-    const void* x;
-    const float* x_scale;
-    int n, cin;
-    const void *packed, *scales, *offsets, *bias;
+    const void *x, *packed, *scales, *offsets, *bias;
     void* out;
-    int cout;
+    W4Params p;
     cudaStream_t stream;
 };
 
-template <typename T, typename X, int MT, int NT, int GROUP>
-void launch_w4_as(const W4Args& a) {
-    const dim3 grid((a.cout + 16 * MT - 1) / (16 * MT), (a.n + 8 * NT - 1) / (8 * NT));
-    const int smem = w4_smem<T, MT, NT>(a.cin / GROUP);
-    if (smem > 48 * 1024)
-        cudaFuncSetAttribute(k_linear_w4<T, X, MT, NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    k_linear_w4<T, X, MT, NT, GROUP><<<grid, 32 * kW4Warps, smem, a.stream>>>(
-        static_cast<const X*>(a.x), a.x_scale, a.n, a.cin, static_cast<const uint32_t*>(a.packed),
-        static_cast<const T*>(a.scales), static_cast<const T*>(a.offsets), static_cast<const T*>(a.bias),
-        static_cast<T*>(a.out), a.cout);
-}
-
-// Outputs a CTA: many of them share one read and conversion of x, as long as every SM
-// still gets a CTA.
-template <typename T, typename X, int NT, int GROUP, int MOST>
-void launch_w4_rows(const W4Args& a) {
+template <typename T, typename X, int NT, int GROUP>
+void launch_w4_rows(W4Args a) {
+    using S = W4Shape<X, NT>;
     constexpr int kSms = 148;
-    if (MOST >= 4 && a.cout >= 64 * kSms)
-        launch_w4_as<T, X, MOST < 4 ? 1 : 4, NT, GROUP>(a);
-    else if (MOST >= 2 && a.cout >= 32 * kSms)
-        launch_w4_as<T, X, MOST < 2 ? 1 : 2, NT, GROUP>(a);
-    else
-        launch_w4_as<T, X, 1, NT, GROUP>(a);
+    // Tiles a CTA: the most that its registers hold, dealt so that the SMs' shares
+    // differ by one tile at most.
+    const int tiles = (a.p.cout + 15) / 16, waves = (tiles + kSms * S::kTiles - 1) / (kSms * S::kTiles);
+    a.p.tiles = (tiles + kSms * waves - 1) / (kSms * waves);
+    // Scales: all groups, or as many rounds of the warps over the chunks as the table takes.
+    const int groups = a.p.cin / GROUP, round = S::kWarps * (S::kChunk < 128 ? 128 : S::kChunk) / GROUP;
+    a.p.seg_groups = groups;
+    while (w4_pitch(a.p.seg_groups, sizeof(T)) * a.p.tiles * 32 > kW4TableBytes && a.p.seg_groups > round)
+        a.p.seg_groups = (a.p.seg_groups / 2 + round - 1) / round * round;
+    a.p.pitch = w4_pitch(a.p.seg_groups, sizeof(T));
+    const int join = S::kWarps * S::kTiles * 16 * (NT * 8 + 1) * 4, work = S::kRingBytes + a.p.pitch * a.p.tiles * 32;
+    const int smem = work > join ? work : join;
+    cudaFuncSetAttribute(k_linear_w4<T, X, NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const dim3 grid((tiles + a.p.tiles - 1) / a.p.tiles, (a.p.n + 8 * NT - 1) / (8 * NT));
+    k_linear_w4<T, X, NT, GROUP><<<grid, S::kThreads, smem, a.stream>>>(
+        static_cast<const X*>(a.x), static_cast<const uint32_t*>(a.packed), static_cast<const T*>(a.scales),
+        static_cast<const T*>(a.offsets), static_cast<const T*>(a.bias), static_cast<T*>(a.out), a.p);
 }
 
-// Rows a CTA: all of them, so that the weights are read once; fp32 rows take three
-// times the registers, and go 16 at a time.
+// Rows a CTA: all of them, so that the weights are read once; fp32 rows go 8 at a time.
 template <typename T, typename X, int GROUP>
 void launch_w4_group(const W4Args& a) {
-    if (a.n <= 8) {
-        launch_w4_rows<T, X, 1, GROUP, sizeof(X) == 4 ? 2 : 4>(a);
-    } else if (a.n <= 16 || sizeof(X) == 4) {
-        launch_w4_rows<T, X, 2, GROUP, sizeof(X) == 4 ? 1 : 2>(a);
-    } else if constexpr (sizeof(X) < 4) {
-        launch_w4_rows<T, X, 4, GROUP, 2>(a);
+    if constexpr (sizeof(X) == 4) {
+        launch_w4_rows<T, X, 1, GROUP>(a);
+    } else {
+        if (a.p.n <= 8)
+            launch_w4_rows<T, X, 1, GROUP>(a);
+        else if (a.p.n <= 16)
+            launch_w4_rows<T, X, 2, GROUP>(a);
+        else
+            launch_w4_rows<T, X, 4, GROUP>(a);
     }
 }
 
@@ -542,7 +576,11 @@ spconv_status_t spconv_linear_w4(spconv_dtype_t dtype, const void* x, const floa
         overlaps(out, ob, packed, pb) || overlaps(out, ob, scales, gb) || overlaps(out, ob, offsets, gb) ||
         overlaps(out, ob, bias, (int64_t)cout * es))
         return row_fail(SPCONV_ERR_INVALID_ARG, "out must not overlap another buffer of the call");
-    const W4Args a = {x, x_scale, (int)n, cin, packed, scales, offsets, bias, out, cout, static_cast<cudaStream_t>(stream)};
+    W4Args a = {x, packed, scales, offsets, bias, out, {}, static_cast<cudaStream_t>(stream)};
+    a.p.x_scale = x_scale;
+    a.p.n = (int)n;
+    a.p.cin = cin;
+    a.p.cout = cout;
     if (dtype == SPCONV_BF16 && x_scale)
         launch_linear_w4<__nv_bfloat16, __nv_fp8_e4m3>(a, group);
     else if (dtype == SPCONV_BF16)
