@@ -15,7 +15,7 @@
 namespace spconv {
 namespace {
 
-// D += A B on a 16 x 8 tile, K = 16, fp32 accumulation.
+// D += A B (or D = A B: _first) on a 16 x 8 tile, K = 16, fp32 accumulation.
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -27,6 +27,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                                __nv_bfloat16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // The codes i and i + 4 of a word as two 16-bit floats, and how the sums over them are
@@ -136,34 +150,31 @@ struct XShare<float, W> {
 };
 
 // A launch's shape.  NT: blocks of 8 rows a CTA holds; then, of the 65,536 registers of
-// an SM, KC input channels of x, 16 MT outputs' sums and the next channels of x fit
-// WARPS warps (fp32 rows take three parts each).
+// an SM, kChunk input channels of x, the sums of MT tiles of 16 outputs and the next
+// channels of x fit kWarps warps (fp32 rows take three parts each).
 template <typename X, int NT>
 struct W4Shape {
     static constexpr int kChunk = NT == 4 || sizeof(X) == 4 ? 64 : 128;
-    static constexpr int kTiles = NT == 4 || sizeof(X) == 4 ? 4 : 8;
+    static constexpr int kMostTiles = NT == 1 && sizeof(X) < 4 ? 8 : 4;
     static constexpr int kWarps = NT == 1 && sizeof(X) < 4 ? 16 : 12;
     static constexpr int kThreads = 32 * kWarps;
-    // steps (a tile of a chunk) of codes on the way: a power of two of them in the ring
-    static constexpr int kRing = 8, kAhead = kRing - 1;
-    static constexpr int kStepBytes = 2 * (kChunk / 8) * kThreads;  // of codes, over all warps
-    static constexpr int kRingBytes = kRing * kStepBytes;
+    static constexpr int kSteps = 8;  // steps (a tile of a chunk) whose codes are on the way
+    static constexpr int kRingBytes = kSteps * 2 * (kChunk / 8) * kThreads;
 };
 constexpr int kW4TableBytes = 72 * 1024;  // scales and offsets held at a time, at most
 
-// Bytes between two outputs' scales in shared memory: 16 more than a multiple of 32, so
-// that eight outputs' reads fall on different banks.
-inline int w4_pitch(int groups, int elem) { return (groups * elem + 31) / 32 * 32 + 16; }
+// A scale and its offset side by side, read with one access.
+template <typename T>
+struct alignas(2 * sizeof(T)) ScaleOffset {
+    T s, z;
+};
 
 template <int BYTES>
-__device__ __forceinline__ void copy_words(void* dst, const void* src, bool in) {
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
-    const int take = in ? BYTES : 0;  // the rest is filled with zeros
+__device__ __forceinline__ void copy_words(uint32_t to, const void* from) {
     if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(take) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(BYTES), "r"(take)
-                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 
 struct W4Params {
@@ -171,78 +182,89 @@ struct W4Params {
     int n, cin, cout;
     int tiles;        // tiles of 16 outputs a CTA
     int seg_groups;   // groups whose scales a CTA holds at a time
-    int pitch;        // bytes between two outputs' scales in shared memory
 };
 
-// A CTA multiplies `tiles` tiles of 16 outputs by 8 NT rows.  A warp takes every
+// A CTA multiplies up to MT tiles of 16 outputs by 8 NT rows.  A warp takes every
 // kWarps-th chunk of the input channels: it holds the chunk's part of x in registers, as
 // the tensor-core operand, and streams the tiles' codes past it; the warps' sums are
-// joined in shared memory at the end.  What bounds it: the codes' way from memory (for
-// more than 16 rows the tensor cores), so the codes of the next seven steps are on
-// their way into shared memory (each thread copies and reads its own words, so no warp
-// waits for another) and the next chunk's x into registers.
+// joined in shared memory at the end.  What bounds it: the instructions that turn codes
+// into operands, then the codes' way from memory.  The codes of the next eight steps are
+// on their way into shared memory (each thread copies and reads its own words, so no
+// warp waits for another) and the next chunk's x into registers.
 //
 // Fragments.  In one 16 x 8 x 16 step lane (g, t) = (lane / 4, lane % 4) holds four
 // input channels of outputs g and g + 8 and of row g; which four is free as long as both
-// operands agree.  A group's scale must be common to the step, so of a part of SUB
+// operands agree.  A group's scale must be common to the step, so of a part of kSub
 // channels (a group, or as much of it as a chunk has) lane t owns the words
-// [t W, t W + W), W = SUB / 32, neighbouring in memory, and each word gives two steps.
+// [t W, t W + W), W = kSub / 32, neighbouring in memory, and each word gives two steps.
+// Channels behind the last are zeros of x, whatever their codes (all codes are finite).
 //
 // Scales.  Over a part the sum of f(q) x is the step's accumulator, started at zero for
 // each part; the sum of x comes out of the same instruction with ones in place of the
 // codes, once for all tiles.  The CTA's scales are brought into shared memory along the
 // groups, as they lie in memory; read per lane from global memory, each of them would
 // cost a cache line's lookup.
-template <typename T, typename X, int NT, int GROUP>
+template <typename T, typename X, int NT, int MT, int GROUP>
 __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     k_linear_w4(const X* __restrict__ x, const uint32_t* __restrict__ packed, const T* __restrict__ scales,
                 const T* __restrict__ offsets, const T* __restrict__ bias, T* __restrict__ out, const W4Params a) {
     using S = W4Shape<X, NT>;
     using C = Codes<X>;
+    using Half = typename C::Half;
     constexpr int kChunk = S::kChunk, kSub = GROUP < kChunk ? GROUP : kChunk, kW = kSub / 32, kSubs = kChunk / kSub;
     constexpr int kLane = kChunk / 32;  // words a lane has of an output's chunk
+    constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRounds = S::kSteps / MT, kPitch = MT * 16 + 1;
     using Share = XShare<X, kW>;
-    constexpr int kParts = Share::kParts, kMt = S::kTiles, kThreads = S::kThreads, kWarps = S::kWarps;
+    constexpr int kParts = Share::kParts;
+    constexpr uint32_t kHalfBytes = kThreads * kLane * 4, kSlotBytes = 2 * kHalfBytes;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint32_t* ring = reinterpret_cast<uint32_t*>(smem) + threadIdx.x * kLane;  // [step][output half][thread][word]
-    unsigned char* table = smem + S::kRingBytes;                              // [scale, offset][output][group]
+    // [slot][output half][thread][word], then [group of the segment][output]
+    unsigned char* ring = smem + threadIdx.x * (kLane * 4);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    ScaleOffset<T>* table = reinterpret_cast<ScaleOffset<T>*>(smem + S::kRingBytes);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int words = a.cin / 8, groups = a.cin / GROUP, chunks = (a.cin + kChunk - 1) / kChunk;
     const int o0 = blockIdx.x * a.tiles * 16, row0 = blockIdx.y * NT * 8;
     const int tiles = min(a.tiles, (a.cout - o0 + 15) / 16);
-    float y[kMt][NT][4];
+    float y[MT][NT][4];
 #pragma unroll
-    for (int m = 0; m < kMt; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[m][b][e] = 0.0f;
 
-    // The codes' way: step after step, tile after tile of a chunk, then the next chunk.
-    int f_tile = 0, f_chunk = warp, f_slot = 0;
-    const auto fetch = [&]() {
-        if (f_chunk < chunks) {
+    // Codes of tile m of a chunk, kRounds rounds before their turn and into the slot that
+    // their turn reads.
+    const int my_outs = a.cout - o0 - g;
+    const int64_t tile_words = 16 * (int64_t)words;
+    const uint32_t* next = packed + (int64_t)(o0 + g) * words + warp * (kChunk / 8) + t * kW;  // this lane's, tile 0
+    int next_word = warp * (kChunk / 8) + t * kW;
+    const auto fetch = [&](int m, int slot) {
+        if (m < tiles) {
+            const uint32_t* from = next + m * tile_words;
+            const uint32_t to = ring_at + slot * kSlotBytes;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int o = o0 + f_tile * 16 + r * 8 + g;
-                uint32_t* to = ring + (f_slot * 2 + r) * (kThreads * kLane);
-#pragma unroll
-                for (int j = 0; j < kSubs; ++j) {
-                    const int word = f_chunk * (kChunk / 8) + j * (kSub / 8) + t * kW;
-                    const bool in = o < a.cout && word < words;
-                    copy_words<4 * kW>(to + j * kW, in ? packed + (int64_t)o * words + word : packed, in);
+            for (int j = 0; j < kSubs; ++j) {
+                if (next_word + j * (kSub / 8) < words) {
+                    if (m * 16 < my_outs) copy_words<4 * kW>(to + j * (kW * 4), from + j * (kSub / 8));
+                    if (m * 16 + 8 < my_outs)
+                        copy_words<4 * kW>(to + kHalfBytes + j * (kW * 4), from + 8 * words + j * (kSub / 8));
                 }
             }
-            if (++f_tile == tiles) {
-                f_tile = 0;
-                f_chunk += kWarps;
-            }
         }
-        f_slot = (f_slot + 1) % S::kRing;
         copy_commit();
     };
+    const auto next_chunk = [&]() {
+        next += kWarps * (kChunk / 8);
+        next_word += kWarps * (kChunk / 8);
+    };
 #pragma unroll
-    for (int s = 0; s < S::kAhead; ++s) fetch();
+    for (int d = 0; d < kRounds; ++d) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) fetch(m, d * MT + m);
+        next_chunk();
+    }
     const auto load_x = [&](Share (&xs)[NT][kSubs], int chunk) {
 #pragma unroll
         for (int b = 0; b < NT; ++b)
@@ -255,25 +277,27 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     Share raw[NT][kSubs];
     load_x(raw, warp);
 
-    int slot = 0, chunk = warp;
+    int base = 0, chunk = warp;  // base: the round's first slot
     for (int seg = 0; seg < groups; seg += a.seg_groups) {
         const int held = min(a.seg_groups, groups - seg), rows = min(tiles * 16, a.cout - o0);
+        const int64_t from = (int64_t)o0 * groups + seg;
         if (seg) __syncthreads();
-        for (int z = 0; z < 2; ++z) {
-            const T* from = (z ? offsets : scales) + (int64_t)o0 * groups + seg;
-            unsigned char* to = table + z * (a.tiles * 16) * a.pitch;
-            constexpr int kVe = 16 / (int)sizeof(T);
-            if (groups % kVe == 0 && seg % kVe == 0) {
-                const int vecs = (held + kVe - 1) / kVe, per = kThreads / 32;
-                for (int o = warp; o < rows; o += per)
-                    for (int v = lane; v < vecs; v += 32)
-                        *reinterpret_cast<uint4*>(to + o * a.pitch + v * 16) =
-                            *reinterpret_cast<const uint4*>(from + (int64_t)o * groups + v * kVe);
-            } else {
-                for (int o = warp; o < rows; o += kThreads / 32)
-                    for (int v = lane; v < held; v += 32)
-                        *reinterpret_cast<T*>(to + o * a.pitch + v * (int)sizeof(T)) = from[(int64_t)o * groups + v];
-            }
+        constexpr int kVe = 16 / (int)sizeof(T);
+        if (groups % kVe == 0 && seg % kVe == 0) {
+            const int vecs = (held + kVe - 1) / kVe;  // (the last may run into the next segment's)
+            for (int o = warp; o < rows; o += kWarps)
+                for (int v = lane; v < vecs; v += 32) {
+                    const Vec<T, kVe> s = load_vec<T, kVe>(scales + from + (int64_t)o * groups + v * kVe);
+                    const Vec<T, kVe> z = load_vec<T, kVe>(offsets + from + (int64_t)o * groups + v * kVe);
+#pragma unroll
+                    for (int e = 0; e < kVe; ++e)
+                        if (v * kVe + e < held) table[(v * kVe + e) * kPitch + o] = ScaleOffset<T>{s.v[e], z.v[e]};
+                }
+        } else {
+            for (int o = warp; o < rows; o += kWarps)
+                for (int k = lane; k < held; k += 32)
+                    table[k * kPitch + o] = ScaleOffset<T>{scales[from + (int64_t)o * groups + k],
+                                                           offsets[from + (int64_t)o * groups + k]};
         }
         __syncthreads();
         for (; chunk < chunks && chunk * kChunk < (seg + held) * GROUP; chunk += kWarps) {
@@ -283,8 +307,6 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
             for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int j = 0; j < kSubs; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[b][j][e] = 0.0f;
                     const uint32_t ones[4] = {C::kOne[0], C::kOne[0], C::kOne[1], C::kOne[1]};
 #pragma unroll
                     for (int i = 0; i < kW; ++i)
@@ -292,75 +314,71 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                         for (int p = 0; p < kParts; ++p) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) pairs[b][j][i][e][p] = raw[b][j].pair(i, e, p);
-                            mma_16816(sum[b][j], ones, pairs[b][j][i][0][p], pairs[b][j][i][1][p], typename C::Half());
-                            mma_16816(sum[b][j], ones, pairs[b][j][i][2][p], pairs[b][j][i][3][p], typename C::Half());
+                            if (i == 0 && p == 0)
+                                mma_16816_first(sum[b][j], ones, pairs[b][j][i][0][p], pairs[b][j][i][1][p], Half());
+                            else
+                                mma_16816(sum[b][j], ones, pairs[b][j][i][0][p], pairs[b][j][i][1][p], Half());
+                            mma_16816(sum[b][j], ones, pairs[b][j][i][2][p], pairs[b][j][i][3][p], Half());
                         }
                 }
             if (chunk + kWarps < chunks) load_x(raw, chunk + kWarps);
-            const int at = chunk * kChunk / GROUP - seg;  // the chunk's first group in the table
+            const ScaleOffset<T>* at[kSubs];
 #pragma unroll
-            for (int m = 0; m < kMt; ++m) {
-                if (m >= tiles) continue;
-                fetch();  // into the slot read in the last step
-                copy_wait<S::kAhead>();
-                uint32_t w[2][kLane];
+            for (int j = 0; j < kSubs; ++j)  // (behind the last group: any scale, the sums are zero)
+                at[j] = table + min(chunk * kChunk / GROUP + j - seg, held - 1) * kPitch + g;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t* from = ring + (slot * 2 + r) * (kThreads * kLane);
-                    if (kLane == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(from);
-                        w[r][0] = v.x, w[r][1] = v.y, w[r][2 % kLane] = v.z, w[r][3 % kLane] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(from);
-                        w[r][0] = v.x, w[r][1] = v.y;
-                    }
-                }
-                slot = (slot + 1) % S::kRing;
+            for (int m = 0; m < MT; ++m) {
+                copy_wait<S::kSteps - 1>();
+                if (m < tiles) {
+                    const unsigned char* from_slot = ring + (base + m) * kSlotBytes;
+                    Vec<uint32_t, kLane> w[2];
+                    w[0] = load_vec<uint32_t, kLane>(reinterpret_cast<const uint32_t*>(from_slot));
+                    w[1] = load_vec<uint32_t, kLane>(reinterpret_cast<const uint32_t*>(from_slot + kHalfBytes));
 #pragma unroll
-                for (int j = 0; j < kSubs; ++j) {
-                    float d[NT][4];
+                    for (int j = 0; j < kSubs; ++j) {
+                        float d[NT][4];
 #pragma unroll
-                    for (int b = 0; b < NT; ++b)
+                        for (int i = 0; i < kW; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) d[b][e] = 0.0f;
+                            for (int h = 0; h < 4; h += 2) {
+                                const uint32_t w0 = w[0].v[j * kW + i], w1 = w[1].v[j * kW + i];
+                                const uint32_t code[4] = {C::pair(w0, h), C::pair(w1, h), C::pair(w0, h + 1), C::pair(w1, h + 1)};
 #pragma unroll
-                    for (int i = 0; i < 2 * kW; ++i) {
-                        const uint32_t code[4] = {C::pair(w[0][j * kW + i / 2], i % 2 * 2), C::pair(w[1][j * kW + i / 2], i % 2 * 2),
-                                                  C::pair(w[0][j * kW + i / 2], i % 2 * 2 + 1),
-                                                  C::pair(w[1][j * kW + i / 2], i % 2 * 2 + 1)};
+                                for (int p = 0; p < kParts; ++p)
 #pragma unroll
-                        for (int p = 0; p < kParts; ++p)
+                                    for (int b = 0; b < NT; ++b) {
+                                        if (i == 0 && h == 0 && p == 0)
+                                            mma_16816_first(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Half());
+                                        else
+                                            mma_16816(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Half());
+                                    }
+                            }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const ScaleOffset<T> v = at[j][m * 16 + r * 8];
+                            const float s = to_f32(v.s), sc = C::scale(s), of = C::offset(s, to_f32(v.z));
 #pragma unroll
                             for (int b = 0; b < NT; ++b)
-                                mma_16816(d[b], code, pairs[b][j][i / 2][i % 2 * 2][p], pairs[b][j][i / 2][i % 2 * 2 + 1][p],
-                                          typename C::Half());
-                    }
-                    // (behind the last group of the last chunk: sums of zero and the pitch's rest)
-                    const int k = min(at + j, held - 1);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const unsigned char* p = table + (m * 16 + r * 8 + g) * a.pitch + k * (int)sizeof(T);
-                        const float s = to_f32(*reinterpret_cast<const T*>(p));
-                        const float z = to_f32(*reinterpret_cast<const T*>(p + a.tiles * 16 * a.pitch));
-                        const float sc = C::scale(s), of = C::offset(s, z);
-#pragma unroll
-                        for (int b = 0; b < NT; ++b)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float& to = y[m][b][2 * r + e];
-                                to = fmaf(sc, d[b][2 * r + e], fmaf(of, sum[b][j][e], to));
-                            }
+                                for (int e = 0; e < 2; ++e) {
+                                    float& to = y[m][b][2 * r + e];
+                                    to = fmaf(sc, d[b][2 * r + e], fmaf(of, sum[b][j][e], to));
+                                }
+                        }
                     }
                 }
+                fetch(m, base + m);  // the slot's codes have been used
             }
+            next_chunk();
+            base = base + MT == S::kSteps ? 0 : base + MT;
         }
     }
     copy_wait<0>();  // the ring becomes the join's memory
     __syncthreads();
-    float (*join)[kMt * 16][NT * 8 + 1] = reinterpret_cast<float (*)[kMt * 16][NT * 8 + 1]>(smem);
+    float (*join)[MT * 16][NT * 8 + 1] = reinterpret_cast<float (*)[MT * 16][NT * 8 + 1]>(smem);
     // accumulator e of lane (g, t): output g + 8 (e / 2), row 2 t + e % 2
 #pragma unroll
-    for (int m = 0; m < kMt; ++m) {
+    for (int m = 0; m < MT; ++m) {
         if (m >= tiles) continue;
 #pragma unroll
         for (int b = 0; b < NT; ++b)
@@ -368,18 +386,16 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
             for (int e = 0; e < 4; ++e) join[warp][m * 16 + (e >> 1) * 8 + g][b * 8 + 2 * t + (e & 1)] = y[m][b][e];
     }
     __syncthreads();
-    const int outs = tiles * 16;
-    for (int r = warp; r < NT * 8 && row0 + r < a.n; r += kWarps) {
-        const float xs = a.x_scale ? a.x_scale[row0 + r] : 1.0f;
-        for (int o = lane; o < outs && o0 + o < a.cout; o += 32) {
+    const int outs = min(tiles * 16, a.cout - o0), live = min(NT * 8, a.n - row0);
+    for (int o = threadIdx.x % (MT * 16); o < outs; o += MT * 16)
+        for (int r = threadIdx.x / (MT * 16); r < live; r += kThreads / (MT * 16)) {
             float v = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) v += join[k][o][r];
-            v *= xs;
+            if (a.x_scale) v *= a.x_scale[row0 + r];
             if (bias) v += to_f32(bias[o0 + o]);
             out[(int64_t)(row0 + r) * a.cout + o0 + o] = from_f32<T>(v);
         }
-    }
 }
 
 // One thread a (group, output): the output index runs fastest, so the reads of w
@@ -456,27 +472,35 @@ struct W4Args {
     cudaStream_t stream;
 };
 
-template <typename T, typename X, int NT, int GROUP>
-void launch_w4_rows(W4Args a) {
+template <typename T, typename X, int NT, int MT, int GROUP>
+void launch_w4_tiles(W4Args a, int tiles) {
     using S = W4Shape<X, NT>;
-    constexpr int kSms = 148;
-    // Tiles a CTA: the most that its registers hold, dealt so that the SMs' shares
-    // differ by one tile at most.
-    const int tiles = (a.p.cout + 15) / 16, waves = (tiles + kSms * S::kTiles - 1) / (kSms * S::kTiles);
-    a.p.tiles = (tiles + kSms * waves - 1) / (kSms * waves);
     // Scales: all groups, or as many rounds of the warps over the chunks as the table takes.
-    const int groups = a.p.cin / GROUP, round = S::kWarps * (S::kChunk < 128 ? 128 : S::kChunk) / GROUP;
-    a.p.seg_groups = groups;
-    while (w4_pitch(a.p.seg_groups, sizeof(T)) * a.p.tiles * 32 > kW4TableBytes && a.p.seg_groups > round)
-        a.p.seg_groups = (a.p.seg_groups / 2 + round - 1) / round * round;
-    a.p.pitch = w4_pitch(a.p.seg_groups, sizeof(T));
-    const int join = S::kWarps * S::kTiles * 16 * (NT * 8 + 1) * 4, work = S::kRingBytes + a.p.pitch * a.p.tiles * 32;
+    constexpr int kEntry = (MT * 16 + 1) * (int)sizeof(ScaleOffset<T>), kMost = kW4TableBytes / kEntry;
+    constexpr int kRound = S::kWarps * 128 / GROUP;
+    static_assert(kMost >= kRound, "a round's scales fit the table");
+    const int groups = a.p.cin / GROUP;
+    a.p.seg_groups = groups <= kMost ? groups : kMost / kRound * kRound;
+    const int join = S::kWarps * MT * 16 * (NT * 8 + 1) * 4, work = S::kRingBytes + a.p.seg_groups * kEntry;
     const int smem = work > join ? work : join;
-    cudaFuncSetAttribute(k_linear_w4<T, X, NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaFuncSetAttribute(k_linear_w4<T, X, NT, MT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     const dim3 grid((tiles + a.p.tiles - 1) / a.p.tiles, (a.p.n + 8 * NT - 1) / (8 * NT));
-    k_linear_w4<T, X, NT, GROUP><<<grid, S::kThreads, smem, a.stream>>>(
+    k_linear_w4<T, X, NT, MT, GROUP><<<grid, S::kThreads, smem, a.stream>>>(
         static_cast<const X*>(a.x), static_cast<const uint32_t*>(a.packed), static_cast<const T*>(a.scales),
         static_cast<const T*>(a.offsets), static_cast<const T*>(a.bias), static_cast<T*>(a.out), a.p);
+}
+
+// Tiles a CTA: the most that its registers hold, dealt so that the SMs' shares differ by
+// one tile at most.  With one or two, the codes of more chunks are on the way.
+template <typename T, typename X, int NT, int GROUP>
+void launch_w4_rows(W4Args a) {
+    constexpr int kSms = 148, kMost = W4Shape<X, NT>::kMostTiles;
+    const int tiles = (a.p.cout + 15) / 16, waves = (tiles + kSms * kMost - 1) / (kSms * kMost);
+    a.p.tiles = (tiles + kSms * waves - 1) / (kSms * waves);
+    if (a.p.tiles <= 2)
+        launch_w4_tiles<T, X, NT, 2, GROUP>(a, tiles);
+    else
+        launch_w4_tiles<T, X, NT, kMost, GROUP>(a, tiles);
 }
 
 // Rows a CTA: all of them, so that the weights are read once; fp32 rows go 8 at a time.
