@@ -155,19 +155,15 @@ struct XShare<float, W> {
 template <typename X, int NT>
 struct W4Shape {
     static constexpr int kChunk = NT == 4 || sizeof(X) == 4 ? 64 : 128;
-    static constexpr int kMostTiles = NT == 1 && sizeof(X) < 4 ? 8 : 4;
-    static constexpr int kWarps = NT == 1 && sizeof(X) < 4 ? 16 : 12;
+    static constexpr int kMostTiles = sizeof(X) == 4 ? 2 : NT == 1 ? 8 : 4;
+    static constexpr int kWarps = sizeof(X) == 4 ? 8 : NT == 1 ? 16 : 12;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSteps = 8;  // steps (a tile of a chunk) whose codes are on the way
     static constexpr int kRingBytes = kSteps * 2 * (kChunk / 8) * kThreads;
 };
-constexpr int kW4TableBytes = 72 * 1024;  // scales and offsets held at a time, at most
-
-// A scale and its offset side by side, read with one access.
-template <typename T>
-struct alignas(2 * sizeof(T)) ScaleOffset {
-    T s, z;
-};
+// Of an output's scales (and offsets) a CTA holds 256 bytes at a time, 16 more apart, so
+// that eight outputs' reads fall on different banks.
+constexpr int kW4SegBytes = 256, kW4Pitch = kW4SegBytes + 16;
 
 template <int BYTES>
 __device__ __forceinline__ void copy_words(uint32_t to, const void* from) {
@@ -177,11 +173,16 @@ __device__ __forceinline__ void copy_words(uint32_t to, const void* from) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 
+// A chunk's scales of one output, read with one access.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) ScaleVec {
+    T v[N];
+};
+
 struct W4Params {
     const float* x_scale;
     int n, cin, cout;
     int tiles;        // tiles of 16 outputs a CTA
-    int seg_groups;   // groups whose scales a CTA holds at a time
 };
 
 // A CTA multiplies up to MT tiles of 16 outputs by 8 NT rows.  A warp takes every
@@ -213,15 +214,16 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     using Half = typename C::Half;
     constexpr int kChunk = S::kChunk, kSub = GROUP < kChunk ? GROUP : kChunk, kW = kSub / 32, kSubs = kChunk / kSub;
     constexpr int kLane = kChunk / 32;  // words a lane has of an output's chunk
-    constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRounds = S::kSteps / MT, kPitch = MT * 16 + 1;
+    constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRounds = S::kSteps / MT, kSeg = kW4SegBytes / (int)sizeof(T);
     using Share = XShare<X, kW>;
     constexpr int kParts = Share::kParts;
     constexpr uint32_t kHalfBytes = kThreads * kLane * 4, kSlotBytes = 2 * kHalfBytes;
     extern __shared__ __align__(16) unsigned char smem[];
-    // [slot][output half][thread][word], then [group of the segment][output]
+    // [slot][output half][thread][word], then [scale, offset][output][group of the segment]
     unsigned char* ring = smem + threadIdx.x * (kLane * 4);
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-    ScaleOffset<T>* table = reinterpret_cast<ScaleOffset<T>*>(smem + S::kRingBytes);
+    unsigned char* table = smem + S::kRingBytes;
+    constexpr int kOffsets = MT * 16 * kW4Pitch;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int words = a.cin / 8, groups = a.cin / GROUP, chunks = (a.cin + kChunk - 1) / kChunk;
     const int o0 = blockIdx.x * a.tiles * 16, row0 = blockIdx.y * NT * 8;
@@ -277,28 +279,34 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     Share raw[NT][kSubs];
     load_x(raw, warp);
 
-    int base = 0, chunk = warp;  // base: the round's first slot
-    for (int seg = 0; seg < groups; seg += a.seg_groups) {
-        const int held = min(a.seg_groups, groups - seg), rows = min(tiles * 16, a.cout - o0);
-        const int64_t from = (int64_t)o0 * groups + seg;
-        if (seg) __syncthreads();
-        constexpr int kVe = 16 / (int)sizeof(T);
-        if (groups % kVe == 0 && seg % kVe == 0) {
-            const int vecs = (held + kVe - 1) / kVe;  // (the last may run into the next segment's)
-            for (int o = warp; o < rows; o += kWarps)
-                for (int v = lane; v < vecs; v += 32) {
-                    const Vec<T, kVe> s = load_vec<T, kVe>(scales + from + (int64_t)o * groups + v * kVe);
-                    const Vec<T, kVe> z = load_vec<T, kVe>(offsets + from + (int64_t)o * groups + v * kVe);
+    // A segment's scales: on their way with the codes, in 16-byte pieces where the rows of
+    // the scales start on such a boundary.
+    const auto fetch_scales = [&](int seg, int held) {
+        const int rows = min(tiles * 16, a.cout - o0);
+        const T* from[2] = {scales + (int64_t)o0 * groups + seg, offsets + (int64_t)o0 * groups + seg};
+        if (groups * (int)sizeof(T) % 16 == 0) {
+            const int pieces = held * (int)sizeof(T) / 16;
+            for (int o = threadIdx.x / 16; o < rows; o += kThreads / 16)
+                for (int e = threadIdx.x % 16; e < pieces; e += 16)
 #pragma unroll
-                    for (int e = 0; e < kVe; ++e)
-                        if (v * kVe + e < held) table[(v * kVe + e) * kPitch + o] = ScaleOffset<T>{s.v[e], z.v[e]};
-                }
+                    for (int z = 0; z < 2; ++z)
+                        copy16_async(table + z * kOffsets + o * kW4Pitch + e * 16,
+                                     reinterpret_cast<const unsigned char*>(from[z] + (int64_t)o * groups) + e * 16);
         } else {
-            for (int o = warp; o < rows; o += kWarps)
-                for (int k = lane; k < held; k += 32)
-                    table[k * kPitch + o] = ScaleOffset<T>{scales[from + (int64_t)o * groups + k],
-                                                           offsets[from + (int64_t)o * groups + k]};
+            for (int o = threadIdx.x / 16; o < rows; o += kThreads / 16)
+                for (int k = threadIdx.x % 16; k < held; k += 16)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+                        reinterpret_cast<T*>(table + z * kOffsets + o * kW4Pitch)[k] = from[z][(int64_t)o * groups + k];
         }
+    };
+    int base = 0, chunk = warp;  // base: the round's first slot
+    for (int seg = 0; seg < groups; seg += kSeg) {
+        const int held = min(kSeg, groups - seg);
+        if (seg) __syncthreads();
+        fetch_scales(seg, held);
+        copy_commit();
+        copy_wait<0>();
         __syncthreads();
         for (; chunk < chunks && chunk * kChunk < (seg + held) * GROUP; chunk += kWarps) {
             uint32_t pairs[NT][kSubs][kW][4][kParts];
@@ -322,10 +330,8 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                         }
                 }
             if (chunk + kWarps < chunks) load_x(raw, chunk + kWarps);
-            const ScaleOffset<T>* at[kSubs];
-#pragma unroll
-            for (int j = 0; j < kSubs; ++j)  // (behind the last group: any scale, the sums are zero)
-                at[j] = table + min(chunk * kChunk / GROUP + j - seg, held - 1) * kPitch + g;
+            const int at = chunk * kChunk / GROUP - seg;  // the chunk's first group in the segment
+            const unsigned char* of_chunk = table + g * kW4Pitch + at * (int)sizeof(T);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 copy_wait<S::kSteps - 1>();
@@ -334,6 +340,13 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                     Vec<uint32_t, kLane> w[2];
                     w[0] = load_vec<uint32_t, kLane>(reinterpret_cast<const uint32_t*>(from_slot));
                     w[1] = load_vec<uint32_t, kLane>(reinterpret_cast<const uint32_t*>(from_slot + kHalfBytes));
+                    ScaleVec<T, kSubs> sv[2], zv[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const unsigned char* p = of_chunk + (m * 16 + r * 8) * kW4Pitch;
+                        sv[r] = *reinterpret_cast<const ScaleVec<T, kSubs>*>(p);
+                        zv[r] = *reinterpret_cast<const ScaleVec<T, kSubs>*>(p + kOffsets);
+                    }
 #pragma unroll
                     for (int j = 0; j < kSubs; ++j) {
                         float d[NT][4];
@@ -353,10 +366,10 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                                             mma_16816(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Half());
                                     }
                             }
+                        if (j > 0 && at + j >= held) continue;  // behind the last group
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const ScaleOffset<T> v = at[j][m * 16 + r * 8];
-                            const float s = to_f32(v.s), sc = C::scale(s), of = C::offset(s, to_f32(v.z));
+                            const float s = to_f32(sv[r].v[j]), sc = C::scale(s), of = C::offset(s, to_f32(zv[r].v[j]));
 #pragma unroll
                             for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -475,14 +488,10 @@ struct W4Args {
 template <typename T, typename X, int NT, int MT, int GROUP>
 void launch_w4_tiles(W4Args a, int tiles) {
     using S = W4Shape<X, NT>;
-    // Scales: all groups, or as many rounds of the warps over the chunks as the table takes.
-    constexpr int kEntry = (MT * 16 + 1) * (int)sizeof(ScaleOffset<T>), kMost = kW4TableBytes / kEntry;
-    constexpr int kRound = S::kWarps * 128 / GROUP;
-    static_assert(kMost >= kRound, "a round's scales fit the table");
-    const int groups = a.p.cin / GROUP;
-    a.p.seg_groups = groups <= kMost ? groups : kMost / kRound * kRound;
-    const int join = S::kWarps * MT * 16 * (NT * 8 + 1) * 4, work = S::kRingBytes + a.p.seg_groups * kEntry;
-    const int smem = work > join ? work : join;
+    static_assert(kW4SegBytes / sizeof(T) % (S::kChunk > GROUP ? S::kChunk / GROUP : 1) == 0, "segments hold whole chunks");
+    constexpr int join = S::kWarps * MT * 16 * (NT * 8 + 1) * 4, work = S::kRingBytes + 2 * MT * 16 * kW4Pitch;
+    constexpr int smem = work > join ? work : join;
+    static_assert(smem <= 227 * 1024, "fits an SM");
     cudaFuncSetAttribute(k_linear_w4<T, X, NT, MT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     const dim3 grid((tiles + a.p.tiles - 1) / a.p.tiles, (a.p.n + 8 * NT - 1) / (8 * NT));
     k_linear_w4<T, X, NT, MT, GROUP><<<grid, S::kThreads, smem, a.stream>>>(
@@ -497,10 +506,10 @@ void launch_w4_rows(W4Args a) {
     constexpr int kSms = 148, kMost = W4Shape<X, NT>::kMostTiles;
     const int tiles = (a.p.cout + 15) / 16, waves = (tiles + kSms * kMost - 1) / (kSms * kMost);
     a.p.tiles = (tiles + kSms * waves - 1) / (kSms * waves);
-    if (a.p.tiles <= 2)
-        launch_w4_tiles<T, X, NT, 2, GROUP>(a, tiles);
-    else
-        launch_w4_tiles<T, X, NT, kMost, GROUP>(a, tiles);
+    if constexpr (kMost > 2) {
+        if (a.p.tiles > 2) return launch_w4_tiles<T, X, NT, kMost, GROUP>(a, tiles);
+    }
+    launch_w4_tiles<T, X, NT, 2, GROUP>(a, tiles);
 }
 
 // Rows a CTA: all of them, so that the weights are read once; fp32 rows go 8 at a time.
