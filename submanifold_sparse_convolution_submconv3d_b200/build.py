@@ -29,7 +29,7 @@ def nvcc_path() -> str:
 
 def flags(verbose_ptxas: bool = False) -> list[str]:
     f = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-         "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+         "--threads", "0", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", os.path.join(ROOT, "include")]
     if verbose_ptxas:
         f += ["-Xptxas", "-v"]

@@ -8,39 +8,37 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include <type_traits>
-
 #include "row_ops.cuh"
 
 namespace spconv {
 namespace {
 
-// D += A B (or D = A B: _first) on a 16 x 8 tile, K = 16, fp32 accumulation.
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D += A B (FIRST: D = A B) on a 16 x 8 tile over 16 channels, with fp32 accumulation.
+template <bool FIRST>
+__device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
+    if (FIRST)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                                __nv_bfloat16) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+template <bool FIRST>
+__device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+    if (FIRST)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The codes i and i + 4 of a word as two 16-bit floats, and how the sums over them are
@@ -50,11 +48,13 @@ __device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&
 // Rows of e4m3 run in fp16, whose numbers under 2^-14 are spaced evenly: the bits of q
 // in the lowest places are q 2^-24, four places up 16 q 2^-24, so a code needs one mask
 // (and every other pair a shift); the pairs four places up meet x / 16, which fp16 holds.
+// (The same in e4m3's own steps of 32 channels would take fewer masks, but those steps run
+// as conversions and two fp16 steps: 19.4 us against 17.6 for 8 rows through 8192 x 16384.)
 template <typename X>
 struct Codes {
-    using Half = __half;
+    using Elem = __half;
     static constexpr uint32_t kOne[2] = {0x3c003c00u, 0x4c004c00u};  // 1 and 16
-    __device__ static uint32_t pair(uint32_t w, int i) {
+    __device__ static uint32_t part(uint32_t w, int i) {
         return (i < 2 ? w : w >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
     }
     __device__ static float scale(float s) { return s * 16777216.0f; }
@@ -64,18 +64,18 @@ struct Codes {
 // at 2^-24 of 128 |x|, far under the 2^-9 of the result.
 template <>
 struct Codes<__nv_bfloat16> {
-    using Half = __nv_bfloat16;
+    using Elem = __nv_bfloat16;
     static constexpr uint32_t kOne[2] = {0x3f803f80u, 0x3f803f80u};
-    __device__ static uint32_t pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+    __device__ static uint32_t part(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
     __device__ static float scale(float s) { return s; }
     __device__ static float offset(float s, float z) { return fmaf(-128.0f, s, z); }
 };
 // Rows of fp32: 136 taken off, exactly, so the sums run on -8 .. 7.
 template <>
 struct Codes<float> {
-    using Half = __nv_bfloat16;
+    using Elem = __nv_bfloat16;
     static constexpr uint32_t kOne[2] = {0x3f803f80u, 0x3f803f80u};
-    __device__ static uint32_t pair(uint32_t w, int i) {
+    __device__ static uint32_t part(uint32_t w, int i) {
         const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
         const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.0f));
         return *reinterpret_cast<const uint32_t*>(&q);
@@ -122,8 +122,8 @@ struct XShare<__nv_fp8_e4m3, W> {
         uint32_t r;
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
         if (i & 1) {  // meets 16 q
-            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(0.0625f));
-            r = *reinterpret_cast<const uint32_t*>(&v);
+            const __half2 v16 = __hmul2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(0.0625f));
+            r = *reinterpret_cast<const uint32_t*>(&v16);
         }
         return r;
     }
@@ -165,20 +165,6 @@ struct W4Shape {
 // that eight outputs' reads fall on different banks.
 constexpr int kW4SegBytes = 256, kW4Pitch = kW4SegBytes + 16;
 
-template <int BYTES>
-__device__ __forceinline__ void copy_words(uint32_t to, const void* from) {
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
-}
-
-// A chunk's scales of one output, read with one access.
-template <typename T, int N>
-struct alignas(sizeof(T) * N) ScaleVec {
-    T v[N];
-};
-
 struct W4Params {
     const float* x_scale;
     int n, cin, cout;
@@ -211,7 +197,8 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                 const T* __restrict__ offsets, const T* __restrict__ bias, T* __restrict__ out, const W4Params a) {
     using S = W4Shape<X, NT>;
     using C = Codes<X>;
-    using Half = typename C::Half;
+    using Elem = typename C::Elem;
+    constexpr int kOps = 4;  // operand registers a word
     constexpr int kChunk = S::kChunk, kSub = GROUP < kChunk ? GROUP : kChunk, kW = kSub / 32, kSubs = kChunk / kSub;
     constexpr int kLane = kChunk / 32;  // words a lane has of an output's chunk
     constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRounds = S::kSteps / MT, kSeg = kW4SegBytes / (int)sizeof(T);
@@ -219,9 +206,15 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     constexpr int kParts = Share::kParts;
     constexpr uint32_t kHalfBytes = kThreads * kLane * 4, kSlotBytes = 2 * kHalfBytes;
     extern __shared__ __align__(16) unsigned char smem[];
-    // [slot][output half][thread][word], then [scale, offset][output][group of the segment]
-    unsigned char* ring = smem + threadIdx.x * (kLane * 4);
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    // [slot][output half][warp][output][words], then [scale, offset][output][group of the segment].
+    // A lane copies the words [t kLane, ...) of its output's chunk and reads words [t W, ...)
+    // of each part; where these differ (groups shorter than the chunk) the lanes of an output
+    // read each other's copies, and its 16-byte pieces change places by the output so that
+    // eight outputs' reads fall on different banks.
+    constexpr bool kShared = kLane == 4 && kW < 4;
+    const int turn = !kShared ? 0 : kW == 2 ? ((threadIdx.x >> 3) & 1) * 2 : (threadIdx.x >> 3) & 3;  // (g >> 1)
+    unsigned char* ring = smem + (threadIdx.x / 4) * (kLane * 16);  // this lane's output's
+    const uint32_t ring_at = shared_at(ring) + ((threadIdx.x & 3) ^ turn) * (kLane * 4);
     unsigned char* table = smem + S::kRingBytes;
     constexpr int kOffsets = MT * 16 * kW4Pitch;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -240,18 +233,19 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     // their turn reads.
     const int my_outs = a.cout - o0 - g;
     const int64_t tile_words = 16 * (int64_t)words;
-    const uint32_t* next = packed + (int64_t)(o0 + g) * words + warp * (kChunk / 8) + t * kW;  // this lane's, tile 0
-    int next_word = warp * (kChunk / 8) + t * kW;
+    constexpr int kCopies = kShared ? 1 : kSubs, kCopy = kLane / kCopies;  // copies an output, words a copy
+    const uint32_t* next = packed + (int64_t)(o0 + g) * words + warp * (kChunk / 8) + t * kCopy;  // this lane's, tile 0
+    int next_word = warp * (kChunk / 8) + t * kCopy;
     const auto fetch = [&](int m, int slot) {
         if (m < tiles) {
             const uint32_t* from = next + m * tile_words;
             const uint32_t to = ring_at + slot * kSlotBytes;
 #pragma unroll
-            for (int j = 0; j < kSubs; ++j) {
+            for (int j = 0; j < kCopies; ++j) {
                 if (next_word + j * (kSub / 8) < words) {
-                    if (m * 16 < my_outs) copy_words<4 * kW>(to + j * (kW * 4), from + j * (kSub / 8));
+                    if (m * 16 < my_outs) copy_async<4 * kCopy>(to + j * (kCopy * 4), from + j * (kSub / 8));
                     if (m * 16 + 8 < my_outs)
-                        copy_words<4 * kW>(to + kHalfBytes + j * (kW * 4), from + 8 * words + j * (kSub / 8));
+                        copy_async<4 * kCopy>(to + kHalfBytes + j * (kCopy * 4), from + 8 * words + j * (kSub / 8));
                 }
             }
         }
@@ -290,7 +284,7 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                 for (int e = threadIdx.x % 16; e < pieces; e += 16)
 #pragma unroll
                     for (int z = 0; z < 2; ++z)
-                        copy16_async(table + z * kOffsets + o * kW4Pitch + e * 16,
+                        copy_async<16>(shared_at(table + z * kOffsets + o * kW4Pitch + e * 16),
                                      reinterpret_cast<const unsigned char*>(from[z] + (int64_t)o * groups) + e * 16);
         } else {
             for (int o = threadIdx.x / 16; o < rows; o += kThreads / 16)
@@ -309,7 +303,7 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
         copy_wait<0>();
         __syncthreads();
         for (; chunk < chunks && chunk * kChunk < (seg + held) * GROUP; chunk += kWarps) {
-            uint32_t pairs[NT][kSubs][kW][4][kParts];
+            uint32_t pairs[NT][kSubs][kW][kOps][kParts];
             float sum[NT][kSubs][4];
 #pragma unroll
             for (int b = 0; b < NT; ++b)
@@ -321,12 +315,14 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
 #pragma unroll
                         for (int p = 0; p < kParts; ++p) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) pairs[b][j][i][e][p] = raw[b][j].pair(i, e, p);
-                            if (i == 0 && p == 0)
-                                mma_16816_first(sum[b][j], ones, pairs[b][j][i][0][p], pairs[b][j][i][1][p], Half());
-                            else
-                                mma_16816(sum[b][j], ones, pairs[b][j][i][0][p], pairs[b][j][i][1][p], Half());
-                            mma_16816(sum[b][j], ones, pairs[b][j][i][2][p], pairs[b][j][i][3][p], Half());
+                            for (int e = 0; e < kOps; ++e) pairs[b][j][i][e][p] = raw[b][j].pair(i, e, p);
+#pragma unroll
+                            for (int h = 0; h < kOps; h += 2) {
+                                if (i == 0 && p == 0 && h == 0)
+                                    mma_tile<true>(sum[b][j], ones, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Elem());
+                                else
+                                    mma_tile<false>(sum[b][j], ones, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Elem());
+                            }
                         }
                 }
             if (chunk + kWarps < chunks) load_x(raw, chunk + kWarps);
@@ -338,14 +334,29 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                 if (m < tiles) {
                     const unsigned char* from_slot = ring + (base + m) * kSlotBytes;
                     Vec<uint32_t, kLane> w[2];
-                    w[0] = load_vec<uint32_t, kLane>(reinterpret_cast<const uint32_t*>(from_slot));
-                    w[1] = load_vec<uint32_t, kLane>(reinterpret_cast<const uint32_t*>(from_slot + kHalfBytes));
-                    ScaleVec<T, kSubs> sv[2], zv[2];
+                    if (kShared) __syncwarp();  // the other lanes' copies have come, too
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (kShared) {
+#pragma unroll
+                            for (int j = 0; j < kSubs; ++j) {
+                                // word j kSub / 8 + t W: the piece of 16 bytes that holds it, and its place there
+                                const int piece = (j * kW + (t * kW) / 4) ^ turn, in = (t * kW) % 4;
+                                const auto v = *reinterpret_cast<const Vec<uint32_t, kW>*>(
+                                    from_slot + r * kHalfBytes + piece * 16 + in * 4);
+#pragma unroll
+                                for (int i = 0; i < kW; ++i) w[r].v[j * kW + i] = v.v[i];
+                            }
+                        } else {
+                            w[r] = *reinterpret_cast<const Vec<uint32_t, kLane>*>(from_slot + r * kHalfBytes + t * (kLane * 4));
+                        }
+                    }
+                    Vec<T, kSubs> sv[2], zv[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const unsigned char* p = of_chunk + (m * 16 + r * 8) * kW4Pitch;
-                        sv[r] = *reinterpret_cast<const ScaleVec<T, kSubs>*>(p);
-                        zv[r] = *reinterpret_cast<const ScaleVec<T, kSubs>*>(p + kOffsets);
+                        sv[r] = *reinterpret_cast<const Vec<T, kSubs>*>(p);
+                        zv[r] = *reinterpret_cast<const Vec<T, kSubs>*>(p + kOffsets);
                     }
 #pragma unroll
                     for (int j = 0; j < kSubs; ++j) {
@@ -353,17 +364,17 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
 #pragma unroll
                         for (int i = 0; i < kW; ++i)
 #pragma unroll
-                            for (int h = 0; h < 4; h += 2) {
+                            for (int h = 0; h < kOps; h += 2) {
                                 const uint32_t w0 = w[0].v[j * kW + i], w1 = w[1].v[j * kW + i];
-                                const uint32_t code[4] = {C::pair(w0, h), C::pair(w1, h), C::pair(w0, h + 1), C::pair(w1, h + 1)};
+                                const uint32_t code[4] = {C::part(w0, h), C::part(w1, h), C::part(w0, h + 1), C::part(w1, h + 1)};
 #pragma unroll
                                 for (int p = 0; p < kParts; ++p)
 #pragma unroll
                                     for (int b = 0; b < NT; ++b) {
                                         if (i == 0 && h == 0 && p == 0)
-                                            mma_16816_first(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Half());
+                                            mma_tile<true>(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Elem());
                                         else
-                                            mma_16816(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Half());
+                                            mma_tile<false>(d[b], code, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Elem());
                                     }
                             }
                         if (j > 0 && at + j >= held) continue;  // behind the last group
@@ -380,6 +391,7 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                         }
                     }
                 }
+                if (kShared) __syncwarp();
                 fetch(m, base + m);  // the slot's codes have been used
             }
             next_chunk();

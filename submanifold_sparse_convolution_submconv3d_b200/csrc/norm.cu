@@ -26,7 +26,7 @@ struct MaxNan {
     __device__ static float f(float a, float b) { return max_nan(a, b); }
 };
 
-// The threads of a CTA in groups of TPR, a group a row at a time: 8 or 32 lanes of a
+// The threads of a CTA in groups of TPR, a group a row at a time: 4 to 32 lanes of a
 // warp, or the whole CTA.
 template <int TPR>
 struct Group {
@@ -64,6 +64,7 @@ template <typename T, int VE, int TPR, int E, bool Q8>
 __global__ void __launch_bounds__(Group<TPR>::kThreads)
     k_rms_norm(const T* x, const T* res, const T* __restrict__ weight, int64_t n, int c, float eps, T* sum_out,
                T* __restrict__ out, float* __restrict__ rstd_out, uint8_t* __restrict__ q, float* __restrict__ scale) {
+    using V = Vec<T, VE>;
     constexpr int kItems = E / VE;
     __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
     const int t = threadIdx.x % TPR;
@@ -76,8 +77,8 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
     for (int k = 0; k < kItems; ++k) {
         const int j = (k * TPR + t) * VE;
         if (live && j < c) {
-            vx[k] = load_vec<T, VE>(x + base + j);
-            if (res) vr[k] = load_vec<T, VE>(res + base + j);
+            vx[k] = load_vec<V>(x + base + j);
+            if (res) vr[k] = load_vec<V>(res + base + j);
         }
     }
     float ss = 0.0f;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
         const int j = (k * TPR + t) * VE;
         if (!live || j >= c) continue;
         Vec<T, VE> w;
-        if (weight) w = load_vec<T, VE>(weight + j);
+        if (weight) w = load_vec<V>(weight + j);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             float& y = h[k * VE + e];
@@ -140,8 +141,10 @@ __global__ void __launch_bounds__(Group<TPR>::kThreads)
                                                         __NV_SATFINITE, __NV_E4M3);
                 if (VE == 8)
                     *reinterpret_cast<uint2*>(q + base + j) = *reinterpret_cast<uint2*>(o);
-                else
+                else if (VE == 4)
                     *reinterpret_cast<uint32_t*>(q + base + j) = *reinterpret_cast<uint32_t*>(o);
+                else
+                    *reinterpret_cast<uint16_t*>(q + base + j) = *reinterpret_cast<uint16_t*>(o);
             }
         }
         if (live && t == 0) scale[i] = s;
@@ -191,11 +194,12 @@ __global__ void __launch_bounds__(kLongThreads)
 
 // CTAs that share the rows of the gradient: a constant, so that the order of the column
 // sums depends on the shape alone.  One CTA of 512 threads an SM; more of them add column
-// sums to join (8,191 x 4096 bf16: 40.4 us with 148 CTAs, 42.8 with 296).
-constexpr int kMaxParts = 148;
-inline int row_parts(int64_t n, int rows) {
+// sums to join (8,191 x 4096 bf16: 40.4 us with 148 CTAs, 42.8 with 296).  Rows that are
+// not fetched ahead run on two, which cover each other's waits.
+constexpr int kParts = 148, kMaxParts = 2 * kParts;
+inline int row_parts(int64_t n, int rows, int most) {
     const int64_t need = (n + rows - 1) / rows;
-    return (int)(need < kMaxParts ? need : kMaxParts);
+    return (int)(need < most ? need : most);
 }
 
 // Sum over the TPR threads of a row group of a CTA that holds several.
@@ -223,11 +227,11 @@ __device__ __forceinline__ float group_sum(float v, float* part, int group) {
     return v;
 }
 
-// Rows of the gradient a thread fetches ahead, in shared memory (16-byte copies of its
-// own elements, so no thread waits for another).
+// Rows of the gradient a thread fetches ahead, in shared memory (copies of its own
+// elements, so no thread waits for another; single bf16 elements are too small to copy).
 constexpr int kAhead = 2, kStages = kAhead + 1;
 template <typename T, int VE, int E>
-constexpr bool kFetchesAhead = VE * sizeof(T) == 16 && E * sizeof(T) <= 32;
+constexpr bool kFetchesAhead = VE * sizeof(T) >= 4 && E * sizeof(T) <= 32;
 template <typename T, int VE, int TPR, int E, bool SUM>
 constexpr int kBackwardSmem =
     kFetchesAhead<T, VE, E> ? kStages * (SUM ? 3 : 2) * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512) : 0;
@@ -237,13 +241,14 @@ constexpr int kBackwardSmem =
 // and wait only within the group; a thread keeps the sums of its columns in registers
 // over all its rows, and the groups' sums are joined in shared memory at the end.
 template <typename T, int VE, int TPR, int E, bool SUM>
-__global__ void __launch_bounds__(TPR > 512 ? TPR : 512)
+__global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 && !kFetchesAhead<T, VE, E> ? 2 : 1)
     k_rms_norm_backward(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
                         const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
                         float* __restrict__ part) {
     using V = Vec<T, VE>;
     constexpr int kThreads = TPR > 512 ? TPR : 512, kRows = kThreads / TPR, kItems = E / VE;
     constexpr bool kFetch = kFetchesAhead<T, VE, E>;
+    constexpr int kBytes = VE * sizeof(T) < 4 ? 4 : VE * (int)sizeof(T);  // (not copied under 4)
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     V* ring = reinterpret_cast<V*>(ring_bytes) + threadIdx.x;  // [stage][dy, h, dsum][item][thread]
     __shared__ float red[2][kThreads / 32];
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512)
         const int j = (k * TPR + t) * VE;
 #pragma unroll
         for (int e = 0; e < VE; ++e) w[k].v[e] = from_f32<T>(1.0f);
-        if (weight && j < c) w[k] = load_vec<T, VE>(weight + j);
+        if (weight && j < c) w[k] = load_vec<V>(weight + j);
     }
     const float by_c = 1.0f / (float)c;
     const int64_t step = (int64_t)gridDim.x * kRows, stride = step * c;
@@ -270,9 +275,9 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512)
             for (int k = 0; k < kItems; ++k) {
                 if ((k * TPR + t) * VE >= c) continue;
                 const int64_t from = at_fetch + k * TPR * VE;
-                copy16_async(to + k * kThreads, dy + from);
-                copy16_async(to + (kItems + k) * kThreads, h + from);
-                if (SUM) copy16_async(to + (2 * kItems + k) * kThreads, dsum + from);
+                copy_async<kBytes>(shared_at(to + k * kThreads), dy + from);
+                copy_async<kBytes>(shared_at(to + (kItems + k) * kThreads), h + from);
+                if (SUM) copy_async<kBytes>(shared_at(to + (2 * kItems + k) * kThreads), dsum + from);
             }
         }
         at_fetch += stride;
@@ -295,9 +300,9 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512)
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             if (!live || (k * TPR + t) * VE >= c) continue;
-            vd[k] = kFetch ? from[k * kThreads] : load_vec<T, VE>(dy + at + k * TPR * VE);
-            vh[k] = kFetch ? from[(kItems + k) * kThreads] : load_vec<T, VE>(h + at + k * TPR * VE);
-            if (SUM) vs[k] = kFetch ? from[(2 * kItems + k) * kThreads] : load_vec<T, VE>(dsum + at + k * TPR * VE);
+            vd[k] = kFetch ? from[k * kThreads] : load_vec<V>(dy + at + k * TPR * VE);
+            vh[k] = kFetch ? from[(kItems + k) * kThreads] : load_vec<V>(h + at + k * TPR * VE);
+            if (SUM) vs[k] = kFetch ? from[(2 * kItems + k) * kThreads] : load_vec<V>(dsum + at + k * TPR * VE);
         }
         float g[E], xh[E], dot = 0.0f;
 #pragma unroll
@@ -332,7 +337,9 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512)
                 o[e] = fmaf(-xh[k * VE + e], mean, g[k * VE + e]);
                 o[e] = SUM ? fmaf(rstd, o[e], ds[e]) : rstd * o[e];
             }
-            store_vec(dx + at + k * TPR * VE, pack<T, VE>(o));
+            V packed;
+            pack(o, packed);
+            store_vec(dx + at + k * TPR * VE, packed);
         }
     }
     cudaTriggerProgrammaticLaunchCompletion();  // the column sums' second step may take its place
@@ -463,7 +470,7 @@ void launch_forward_as(const NormArgs& a) {
 template <typename T, int VE, int TPR, int E, bool SUM>
 int launch_backward_sum(const NormArgs& a) {
     constexpr int kThreads = TPR > 512 ? TPR : 512, kSmem = kBackwardSmem<T, VE, TPR, E, SUM>;
-    const int parts = row_parts(a.n, kThreads / TPR);
+    const int parts = row_parts(a.n, kThreads / TPR, kFetchesAhead<T, VE, E> ? kParts : kMaxParts);
     if (kSmem > 48 * 1024 - 16640)  // with the static arrays over what a launch has without asking
         cudaFuncSetAttribute(k_rms_norm_backward<T, VE, TPR, E, SUM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     k_rms_norm_backward<T, VE, TPR, E, SUM><<<parts, kThreads, kSmem, a.stream>>>(
@@ -478,6 +485,16 @@ int launch_backward_as(const NormArgs& a) {
     return a.dsum ? launch_backward_sum<T, VE, TPR, E, true>(a) : launch_backward_sum<T, VE, TPR, E, false>(a);
 }
 
+// Rows that do not start on 16-byte boundaries: two elements at a time, or one.
+template <typename T, int VE, bool Q8>
+void launch_forward_narrow(const NormArgs& a) {
+    if (a.c <= 256) launch_forward_as<T, VE, 16, 16, Q8>(a);
+    else if (a.c <= 512) launch_forward_as<T, VE, 32, 16, Q8>(a);
+    else if (a.c <= 1024) launch_forward_as<T, VE, 128, 8, Q8>(a);
+    else if (a.c <= 4096) launch_forward_as<T, VE, 512, 8, Q8>(a);
+    else launch_forward_as<T, VE, 1024, 32, Q8>(a);
+}
+
 // A thread holds up to 32 elements of a row; the fewest threads that hold it take it.
 template <typename T, bool Q8>
 void launch_forward(const NormArgs& a) {
@@ -487,7 +504,7 @@ void launch_forward(const NormArgs& a) {
             static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.c, a.eps,
             static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
     } else if (a.c % kVe == 0) {
-        if (a.c <= 64) launch_forward_as<T, kVe, 8, 8, Q8>(a);
+        if (a.c <= 64) launch_forward_as<T, kVe, 4, 16, Q8>(a);
         else if (a.c <= 128) launch_forward_as<T, kVe, 8, 16, Q8>(a);
         else if (a.c <= 256) launch_forward_as<T, kVe, 8, 32, Q8>(a);
         else if (a.c <= 512) launch_forward_as<T, kVe, 32, 16, Q8>(a);
@@ -497,13 +514,21 @@ void launch_forward(const NormArgs& a) {
         else if (a.c <= 8192) launch_forward_as<T, kVe, 256, 32, Q8>(a);
         else if (a.c <= 16384) launch_forward_as<T, kVe, 512, 32, Q8>(a);
         else launch_forward_as<T, kVe, 1024, 32, Q8>(a);
+    } else if (a.c % 2 == 0) {
+        launch_forward_narrow<T, 2, Q8>(a);
     } else {
-        if (a.c <= 256) launch_forward_as<T, 1, 32, 8, Q8>(a);
-        else if (a.c <= 512) launch_forward_as<T, 1, 32, 16, Q8>(a);
-        else if (a.c <= 1024) launch_forward_as<T, 1, 32, 32, Q8>(a);
-        else if (a.c <= 4096) launch_forward_as<T, 1, 128, 32, Q8>(a);
-        else launch_forward_as<T, 1, 1024, 32, Q8>(a);
+        launch_forward_narrow<T, 1, Q8>(a);
     }
+}
+
+template <typename T, int VE>
+int launch_backward_narrow(const NormArgs& a) {
+    constexpr int kE = VE * sizeof(T) < 4 ? 8 : 32 / (int)sizeof(T);  // single bf16: nothing on the way
+    if (a.c <= 16 * kE) return launch_backward_as<T, VE, 16, kE>(a);
+    if (a.c <= 32 * kE) return launch_backward_as<T, VE, 32, kE>(a);
+    if (a.c <= 128 * kE) return launch_backward_as<T, VE, 128, kE>(a);
+    if (a.c <= 512 * kE) return launch_backward_as<T, VE, 512, kE>(a);
+    return launch_backward_as<T, VE, 1024, 32>(a);
 }
 
 // 32 bytes of a row a thread (bf16: 16 elements, fp32: 8), then more.
@@ -511,7 +536,7 @@ template <typename T>
 int launch_backward(const NormArgs& a) {
     constexpr int kVe = 16 / (int)sizeof(T);
     if (a.c > 32768) {
-        const int parts = row_parts(a.n, 1);
+        const int parts = row_parts(a.n, 1, kMaxParts);
         k_rms_norm_backward_long<T><<<parts, kLongThreads, 0, a.stream>>>(
             static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
             static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
@@ -519,6 +544,7 @@ int launch_backward(const NormArgs& a) {
     }
     if (a.c % kVe == 0) {
         constexpr int kE = 32 / (int)sizeof(T);
+        if (a.c <= 4 * kE) return launch_backward_as<T, kVe, 4, kE>(a);
         if (a.c <= 8 * kE) return launch_backward_as<T, kVe, 8, kE>(a);
         if (a.c <= 16 * kE) return launch_backward_as<T, kVe, 16, kE>(a);
         if (a.c <= 32 * kE) return launch_backward_as<T, kVe, 32, kE>(a);
@@ -529,10 +555,7 @@ int launch_backward(const NormArgs& a) {
         if (a.c <= 16384) return launch_backward_as<T, kVe, 512, 32>(a);
         return launch_backward_as<T, kVe, 1024, 32>(a);
     }
-    if (a.c <= 256) return launch_backward_as<T, 1, 32, 8>(a);
-    if (a.c <= 1024) return launch_backward_as<T, 1, 128, 8>(a);
-    if (a.c <= 4096) return launch_backward_as<T, 1, 512, 8>(a);
-    return launch_backward_as<T, 1, 1024, 32>(a);
+    return a.c % 2 == 0 ? launch_backward_narrow<T, 2>(a) : launch_backward_narrow<T, 1>(a);
 }
 
 spconv_status_t norm_args(spconv_dtype_t dtype, const void* x, const void* residual, const void* weight, int64_t n,
@@ -615,7 +638,7 @@ spconv_status_t spconv_rms_norm_workspace(int64_t n, int32_t channels, int64_t* 
     if (n < 0 || n >= (int64_t(1) << 31)) return row_fail(SPCONV_ERR_INVALID_ARG, "n must be in [0, 2^31)");
     if (channels < 1 || channels > SPCONV_NORM_MAX_CHANNELS)
         return row_fail(SPCONV_ERR_INVALID_ARG, "channels must be in [1, 65536]");
-    *bytes = (int64_t)row_parts(n, 1) * channels * 4;
+    *bytes = (int64_t)row_parts(n, 1, kMaxParts) * channels * 4;
     return SPCONV_OK;
 }
 
@@ -637,7 +660,7 @@ spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, c
     if (dweight && (!workspace || !is_aligned(workspace, 16)))
         return row_fail(SPCONV_ERR_INVALID_ARG, "dweight needs a 16-byte aligned workspace");
     const int64_t wbytes = (int64_t)channels * dtype_bytes(dtype), bytes = n * wbytes;
-    const int64_t wsbytes = (int64_t)row_parts(n, 1) * channels * 4, dwbytes = (int64_t)channels * 4;
+    const int64_t wsbytes = (int64_t)row_parts(n, 1, kMaxParts) * channels * 4, dwbytes = (int64_t)channels * 4;
     const void* ws = dweight ? workspace : nullptr;
     bool bad = dx != dsum && overlaps(dx, bytes, dsum, bytes);
     bad = bad || overlaps(dx, bytes, dy, bytes) || overlaps(dx, bytes, h, bytes) || overlaps(dx, bytes, weight, wbytes) ||

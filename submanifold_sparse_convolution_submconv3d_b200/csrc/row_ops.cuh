@@ -49,23 +49,24 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// VE elements at a time: one 16-byte access, or single elements at any address.
-template <typename T, int VE>
-struct alignas(sizeof(T) * VE == 16 ? 16 : sizeof(T)) Vec {
+// VE neighbouring elements, read and written with one access where they are aligned to
+// their size, as single elements with a smaller ALIGN.
+template <typename T, int VE, int ALIGN = (int)sizeof(T) * VE>
+struct alignas(ALIGN) Vec {
     T v[VE];
 };
-template <typename T, int VE>
-__device__ __forceinline__ Vec<T, VE> load_vec(const T* p) {
-    return *reinterpret_cast<const Vec<T, VE>*>(p);
+template <typename V, typename T>
+__device__ __forceinline__ V load_vec(const T* p) {
+    return *reinterpret_cast<const V*>(p);
 }
-template <typename T, int VE>
-__device__ __forceinline__ void store_vec(T* p, const Vec<T, VE>& v) {
-    *reinterpret_cast<Vec<T, VE>*>(p) = v;
+template <typename V, typename T>
+__device__ __forceinline__ void store_vec(T* p, const V& v) {
+    *reinterpret_cast<V*>(p) = v;
 }
 
 // The elements as fp32 and back, bf16 two at a time.
-template <typename T, int VE>
-__device__ __forceinline__ void unpack(const Vec<T, VE>& v, float* f) {
+template <typename T, int VE, int A>
+__device__ __forceinline__ void unpack(const Vec<T, VE, A>& v, float* f) {
     if constexpr (sizeof(T) == 2 && VE % 2 == 0) {
 #pragma unroll
         for (int e = 0; e < VE; e += 2) {
@@ -78,9 +79,8 @@ __device__ __forceinline__ void unpack(const Vec<T, VE>& v, float* f) {
         for (int e = 0; e < VE; ++e) f[e] = to_f32(v.v[e]);
     }
 }
-template <typename T, int VE>
-__device__ __forceinline__ Vec<T, VE> pack(const float* f) {
-    Vec<T, VE> v;
+template <typename T, int VE, int A>
+__device__ __forceinline__ void pack(const float* f, Vec<T, VE, A>& v) {
     if constexpr (sizeof(T) == 2 && VE % 2 == 0) {
 #pragma unroll
         for (int e = 0; e < VE; e += 2) {
@@ -92,13 +92,16 @@ __device__ __forceinline__ Vec<T, VE> pack(const float* f) {
 #pragma unroll
         for (int e = 0; e < VE; ++e) v.v[e] = from_f32<T>(f[e]);
     }
-    return v;
 }
 
-// 16 bytes from global to shared memory, asynchronously; groups complete in order.
-__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
+// 4, 8 or 16 bytes from global to shared memory, asynchronously; groups complete in order.
+__device__ __forceinline__ uint32_t shared_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
