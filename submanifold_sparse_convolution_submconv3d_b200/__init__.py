@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -460,10 +461,11 @@ def spconv_subdivide(coords: torch.Tensor, extent, x: torch.Tensor | None = None
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _elsewhere(x: torch.Tensor, stream) -> bool:
-    return stream is not None or x.device.index != torch.cuda.current_device()
+    return stream is not None or x.get_device() != _device_now()
 
 
 @contextlib.contextmanager
@@ -484,8 +486,9 @@ def _on(device: torch.device, stream):
 
 def _in(t: torch.Tensor) -> torch.Tensor:
     """An input as the library reads it: contiguous, on a 16-byte boundary."""
-    t = t.contiguous()
-    return t if t.data_ptr() & 15 == 0 else t.clone()
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 def _ptr(t: torch.Tensor | None):
@@ -493,7 +496,7 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _like(t, shape, dtype, device, what: str) -> None:
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be a {str(dtype)[6:]} tensor {list(shape)} on {device}; got "
                          f"{str(t.dtype)[6:]} {list(t.shape)} on {t.device}")
 
@@ -573,6 +576,13 @@ def spconv_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, resi
     return (out, scale) if residual is None else (out, scale, sum_out)
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(n: int, c: int) -> int:
+    size = ctypes.c_int64()
+    _check(lib.spconv_rms_norm_workspace(n, c, ctypes.byref(size)))
+    return size.value
+
+
 def spconv_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
                              dsum: torch.Tensor | None = None, dx: torch.Tensor | None = None,
                              weight_grad: bool = True, stream=None):
@@ -597,9 +607,7 @@ def spconv_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
     if weight is not None:
         weight = _in(weight)
         if weight_grad:
-            size = ctypes.c_int64()
-            _check(lib.spconv_rms_norm_workspace(n, c, ctypes.byref(size)))
-            workspace = rstd.new_empty(size.value // 4)
+            workspace = rstd.new_empty(_norm_workspace(n, c) // 4)
             dweight = rstd.new_empty(c)
     _check(lib.spconv_rms_norm_backward(_DTYPES[h.dtype], dy.data_ptr(), h.data_ptr(), _ptr(weight), rstd.data_ptr(),
                                         _ptr(dsum), n, c, dx.data_ptr(), _ptr(dweight), _ptr(workspace),

@@ -504,7 +504,8 @@ void launch_w4_tiles(W4Args a, int tiles) {
     constexpr int join = S::kWarps * MT * 16 * (NT * 8 + 1) * 4, work = S::kRingBytes + 2 * MT * 16 * kW4Pitch;
     constexpr int smem = work > join ? work : join;
     static_assert(smem <= 227 * 1024, "fits an SM");
-    cudaFuncSetAttribute(k_linear_w4<T, X, NT, MT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    if (allow_smem(k_linear_w4<T, X, NT, MT, GROUP>, smem, done) != cudaSuccess) return;  // the caller asks why
     const dim3 grid((tiles + a.p.tiles - 1) / a.p.tiles, (a.p.n + 8 * NT - 1) / (8 * NT));
     k_linear_w4<T, X, NT, MT, GROUP><<<grid, S::kThreads, smem, a.stream>>>(
         static_cast<const X*>(a.x), static_cast<const uint32_t*>(a.packed), static_cast<const T*>(a.scales),
@@ -515,7 +516,7 @@ void launch_w4_tiles(W4Args a, int tiles) {
 // one tile at most.  With one or two, the codes of more chunks are on the way.
 template <typename T, typename X, int NT, int GROUP>
 void launch_w4_rows(W4Args a) {
-    constexpr int kSms = 148, kMost = W4Shape<X, NT>::kMostTiles;
+    constexpr int kMost = W4Shape<X, NT>::kMostTiles;
     const int tiles = (a.p.cout + 15) / 16, waves = (tiles + kSms * kMost - 1) / (kSms * kMost);
     a.p.tiles = (tiles + kSms * waves - 1) / (kSms * waves);
     if constexpr (kMost > 2) {

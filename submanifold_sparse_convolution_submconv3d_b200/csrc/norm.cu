@@ -333,8 +333,11 @@ __global__ void __launch_bounds__(kLongThreads)
 // sums depends on the shape alone.  One CTA of 512 threads an SM; more of them add column
 // sums to join (8,191 x 4096 bf16: 40.4 us with 148 CTAs, 42.8 with 296).  Rows that are
 // not fetched ahead run on two, which cover each other's waits.
-constexpr int kParts = 148, kMaxParts = 2 * kParts;
+constexpr int kParts = kSms, kMaxParts = 2 * kParts;
 inline int row_parts(int64_t n, int rows, int most) {
+    // Up to four turns of one CTA: its column sums are the result, and the second step's
+    // launch (3 us on the host, 2 on the GPU) falls away.
+    if (n <= 4 * rows) return 1;
     const int64_t need = (n + rows - 1) / rows;
     return (int)(need < most ? need : most);
 }
@@ -562,7 +565,7 @@ struct NormArgs {
     const void* dsum;
     const float* rstd_in;
     void* dx;
-    float* part;
+    float *dweight, *part;
     cudaStream_t stream;
 };
 
@@ -578,11 +581,14 @@ template <typename T, int VE, int TPR, int E, bool SUM>
 int launch_backward_sum(const NormArgs& a) {
     constexpr int kThreads = TPR > 512 ? TPR : 512, kSmem = kBackwardSmem<T, VE, TPR, E, SUM>;
     const int parts = row_parts(a.n, kThreads / TPR, kFetchesAhead<T, VE, E> ? kParts : kMaxParts);
-    if (kSmem > 48 * 1024 - 16640)  // with the static arrays over what a launch has without asking
-        cudaFuncSetAttribute(k_rms_norm_backward<T, VE, TPR, E, SUM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    float* part = parts == 1 ? a.dweight : a.part;
+    if (kSmem > 0) {
+        static std::atomic<uint64_t> done{0};
+        if (allow_smem(k_rms_norm_backward<T, VE, TPR, E, SUM>, kSmem, done) != cudaSuccess) return 0;  // the caller asks why
+    }
     k_rms_norm_backward<T, VE, TPR, E, SUM><<<parts, kThreads, kSmem, a.stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
-        static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
+        static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), part);
     return parts;
 }
 
@@ -590,7 +596,8 @@ template <typename T, int TPR, bool Q8, bool RES>
 void launch_ring_as(const NormArgs& a) {
     constexpr int VE = 16 / (int)sizeof(T), E = 32 / (int)sizeof(T), kRows = kRingThreads / TPR, kSmem = kForwardSmem<T, E, RES>, kTurns = 12;
     const int64_t blocks = (a.n + kRows - 1) / kRows, most = blocks / kTurns > 2 * kParts ? blocks / kTurns : 2 * kParts;
-    cudaFuncSetAttribute(k_rms_norm_ring<T, VE, TPR, E, Q8, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> done{0};
+    if (allow_smem(k_rms_norm_ring<T, VE, TPR, E, Q8, RES>, kSmem, done) != cudaSuccess) return;  // the caller asks why
     k_rms_norm_ring<T, VE, TPR, E, Q8, RES><<<(unsigned)(blocks < most ? blocks : most), kRingThreads, kSmem, a.stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.n, a.c, a.eps,
         static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
@@ -671,7 +678,7 @@ int launch_backward(const NormArgs& a) {
         const int parts = row_parts(a.n, 1, kMaxParts);
         k_rms_norm_backward_long<T><<<parts, kLongThreads, 0, a.stream>>>(
             static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
-            static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), a.part);
+            static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), parts == 1 ? a.dweight : a.part);
         return parts;
     }
     if (a.c % kVe == 0) {
@@ -770,7 +777,7 @@ spconv_status_t spconv_rms_norm_workspace(int64_t n, int32_t channels, int64_t* 
     if (n < 0 || n >= (int64_t(1) << 31)) return row_fail(SPCONV_ERR_INVALID_ARG, "n must be in [0, 2^31)");
     if (channels < 1 || channels > SPCONV_NORM_MAX_CHANNELS)
         return row_fail(SPCONV_ERR_INVALID_ARG, "channels must be in [1, 65536]");
-    *bytes = (int64_t)row_parts(n, 1, kMaxParts) * channels * 4;
+    *bytes = (int64_t)(n < kMaxParts ? n : kMaxParts) * channels * 4;
     return SPCONV_OK;
 }
 
@@ -792,7 +799,7 @@ spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, c
     if (dweight && (!workspace || !is_aligned(workspace, 16)))
         return row_fail(SPCONV_ERR_INVALID_ARG, "dweight needs a 16-byte aligned workspace");
     const int64_t wbytes = (int64_t)channels * dtype_bytes(dtype), bytes = n * wbytes;
-    const int64_t wsbytes = (int64_t)row_parts(n, 1, kMaxParts) * channels * 4, dwbytes = (int64_t)channels * 4;
+    const int64_t wsbytes = (int64_t)(n < kMaxParts ? n : kMaxParts) * channels * 4, dwbytes = (int64_t)channels * 4;
     const void* ws = dweight ? workspace : nullptr;
     bool bad = dx != dsum && overlaps(dx, bytes, dsum, bytes);
     bad = bad || overlaps(dx, bytes, dy, bytes) || overlaps(dx, bytes, h, bytes) || overlaps(dx, bytes, weight, wbytes) ||
@@ -814,11 +821,12 @@ spconv_status_t spconv_rms_norm_backward(spconv_dtype_t dtype, const void* dy, c
     a.dsum = dsum;
     a.rstd_in = rstd;
     a.dx = dx;
+    a.dweight = dweight;
     a.part = dweight ? static_cast<float*>(workspace) : nullptr;
     a.stream = st;
     const int parts = dtype == SPCONV_BF16 ? launch_backward<__nv_bfloat16>(a) : launch_backward<float>(a);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && dweight) e = launch_dw(a.part, parts, channels, dweight, st);
+    if (e == cudaSuccess && dweight && parts > 1) e = launch_dw(a.part, parts, channels, dweight, st);
     return e == cudaSuccess ? SPCONV_OK : row_fail_cuda(e, "spconv_rms_norm_backward");
 }
 

@@ -159,17 +159,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     }
 }
 
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 148;
-    return sms;
-}
-
 template <typename T, int VE, bool HALVES>
 void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cudaStream_t st) {
     constexpr int kN = kPasses<HALVES>, kWarps = kRopeThreads / 32, kSmem = kRopeSmem<T, VE>, kVoxels = 12;
-    const int sms = device_sms();
     a.chunks = a.pairs / (HALVES ? VE : VE / 2);
     a.chunk_blocks = (a.chunks + 31) / 32;
     a.lanes_head = a.chunks < 32 ? a.chunks : 32;
@@ -186,7 +178,7 @@ void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cud
     const int64_t warps = (a.n + a.voxel_slots - 1) / a.voxel_slots * a.chunk_blocks;
     const int passes = (a.heads + a.head_slots - 1) / a.head_slots;
     int groups = (passes + kN - 1) / kN;
-    if (warps * groups < (int64_t)sms * 2 * kWarps || groups * a.chunk_blocks > 65535) groups = passes;
+    if (warps * groups < (int64_t)kSms * 2 * kWarps || groups * a.chunk_blocks > 65535) groups = passes;
     const int per = (passes + groups - 1) / groups;
     a.unit_heads = per * a.head_slots;
     groups = (passes + per - 1) / per;
@@ -195,10 +187,12 @@ void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cud
     // closer than fewer with more voxels: 273,995 voxels of 12 x 64 in bf16 take 158 us on
     // 4 CTAs an SM and 137 us on 32 (7 voxels a warp), 16,934 of 8 x 96 in fp32 20.8 us at
     // 7 voxels a warp and 26.8 us at 2.
-    const int64_t resident = ((int64_t)sms * 4 + groups * a.chunk_blocks - 1) / (groups * a.chunk_blocks);
+    const int64_t resident = ((int64_t)kSms * 4 + groups * a.chunk_blocks - 1) / (groups * a.chunk_blocks);
     const int64_t most = blocks / kVoxels > resident ? blocks / kVoxels : resident;
-    if (kSmem + (int)sizeof(uint64_t) * kMaxPairs > 48 * 1024)
-        cudaFuncSetAttribute(k_rope<T, VE, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (kSmem > 0) {
+        static std::atomic<uint64_t> done{0};
+        if (allow_smem(k_rope<T, VE, HALVES>, kSmem, done) != cudaSuccess) return;  // the caller asks why
+    }
     k_rope<T, VE, HALVES><<<dim3((unsigned)(blocks < most ? blocks : most), groups * a.chunk_blocks), kRopeThreads, kSmem,
                             st>>>(tab, a, static_cast<const T*>(x), static_cast<T*>(out));
 }

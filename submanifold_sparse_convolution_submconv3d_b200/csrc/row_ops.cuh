@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "common.cuh"
@@ -35,6 +36,23 @@ inline bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbyte
     if (!a || !b) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + (uintptr_t)bbytes && y < x + (uintptr_t)abytes;
+}
+
+// The GPU this library is built for; the launches deal their work by it.
+constexpr int kSms = 148;
+
+// Lets a kernel have `bytes` of dynamic shared memory, once a device (the call costs a
+// good part of a microsecond, a launch three).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (e == cudaSuccess && (dev > 63 || !(done.load(std::memory_order_acquire) & bit))) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    }
+    return e;
 }
 
 inline bool dtype_ok(spconv_dtype_t t) { return t == SPCONV_F32 || t == SPCONV_BF16; }
