@@ -57,6 +57,20 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
     return v;
 }
 
+// The 8-bit form of a row's values with the scale's reciprocal.
+template <int VE>
+__device__ __forceinline__ void store_e4m3(uint8_t* q, const float* y, float inv) {
+    if constexpr (VE == 1) {
+        *q = __nv_cvt_float_to_fp8(y[0] * inv, __NV_SATFINITE, __NV_E4M3);
+    } else {
+        Vec<__nv_fp8x2_storage_t, VE / 2> o;
+#pragma unroll
+        for (int e = 0; e < VE; e += 2)
+            o.v[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y[e] * inv, y[e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        store_vec(q, o);
+    }
+}
+
 // Joins v over the TPR threads of a row group of a CTA that holds several, which wait for
 // each other alone.
 template <typename Op, int TPR>
@@ -88,20 +102,6 @@ __device__ __forceinline__ float group_reduce(float v, float* part, int group) {
 constexpr int kAhead = 2, kStages = kAhead + 1;
 template <typename T, int VE, int E>
 constexpr bool kFetchesAhead = VE * sizeof(T) >= 4 && E * sizeof(T) <= 32;
-
-// The 8-bit form of a row's values with the scale's reciprocal.
-template <int VE>
-__device__ __forceinline__ void store_e4m3(uint8_t* q, const float* y, float inv) {
-    if constexpr (VE == 1) {
-        *q = __nv_cvt_float_to_fp8(y[0] * inv, __NV_SATFINITE, __NV_E4M3);
-    } else {
-        Vec<__nv_fp8x2_storage_t, VE / 2> o;
-#pragma unroll
-        for (int e = 0; e < VE; e += 2)
-            o.v[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y[e] * inv, y[e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        store_vec(q, o);
-    }
-}
 
 constexpr int kRingThreads = 512;
 template <typename T, int E, bool RES>
@@ -211,80 +211,76 @@ __global__ void __launch_bounds__(kRingThreads, 2)
 // A row lives in its threads' registers: E elements each, in items of VE, item k of
 // thread t at (k * TPR + t) * VE.  One read of x and the residual, one write of each
 // result.
-template <typename T, int VE, int TPR, int E, bool Q8>
+template <typename T, int VE, int TPR, int E, bool Q8, bool RES>
 __global__ void __launch_bounds__(Group<TPR>::kThreads)
     k_rms_norm(const T* x, const T* res, const T* __restrict__ weight, int64_t n, int c, float eps, T* sum_out,
                T* __restrict__ out, float* __restrict__ rstd_out, uint8_t* __restrict__ q, float* __restrict__ scale) {
     using V = Vec<T, VE>;
-    constexpr int kItems = E / VE;
+    constexpr int kItems = E / VE, kStep = TPR * VE;
     __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
     const int t = threadIdx.x % TPR;
     const int64_t i = (int64_t)blockIdx.x * Group<TPR>::kRows + threadIdx.x / TPR;
     const bool live = i < n;  // a warp's rows join their sums together, so none leaves early
-    const int64_t base = i * c;
-    float h[E];
-    Vec<T, VE> vx[kItems], vr[kItems];
+    const int64_t at = i * c + t * VE;
+    const int left = live ? c - t * VE : 0;  // item k is in the row where k * kStep < left
+    V vx[kItems], vr[RES ? kItems : 1];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-        const int j = (k * TPR + t) * VE;
-        if (live && j < c) {
-            vx[k] = load_vec<V>(x + base + j);
-            if (res) vr[k] = load_vec<V>(res + base + j);
+        if (k * kStep >= left) continue;
+        vx[k] = load_vec<V>(x + at + k * kStep);
+        if (RES) vr[RES ? k : 0] = load_vec<V>(res + at + k * kStep);
+    }
+    float h[E], ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            float v = k * kStep < left ? to_f32(vx[k].v[e]) : 0.0f;
+            if (RES) v += k * kStep < left ? to_f32(vr[RES ? k : 0].v[e]) : 0.0f;
+            h[k * VE + e] = v;
+            ss = fmaf(v, v, ss);
         }
     }
-    float ss = 0.0f;
+    if (RES && sum_out) {
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int j = (k * TPR + t) * VE;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) h[k * VE + e] = 0.0f;
-        if (live && j < c) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                float v = to_f32(vx[k].v[e]);
-                if (res) v += to_f32(vr[k].v[e]);
-                h[k * VE + e] = v;
-                ss += v * v;
-            }
-            if (sum_out) {
-                Vec<T, VE> o;
-#pragma unroll
-                for (int e = 0; e < VE; ++e) o.v[e] = from_f32<T>(h[k * VE + e]);
-                *reinterpret_cast<Vec<T, VE>*>(sum_out + base + j) = o;
-            }
+        for (int k = 0; k < kItems; ++k) {
+            if (k * kStep >= left) continue;
+            V o;
+            pack(h + k * VE, o);
+            store_vec(sum_out + at + k * kStep, o);
         }
     }
     const float rstd = rsqrtf(row_reduce<Sum, TPR>(ss, part[0]) / (float)c + eps);
-    float m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int j = (k * TPR + t) * VE;
-        if (!live || j >= c) continue;
-        Vec<T, VE> w;
-        if (weight) w = load_vec<V>(weight + j);
+    for (int e = 0; e < E; ++e) h[e] *= rstd;
+    if (weight) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            float& y = h[k * VE + e];
-            y = y * rstd * (weight ? to_f32(w.v[e]) : 1.0f);
-            if (Q8) m = max_nan(m, fabsf(y));
-        }
-        if (!Q8) {
-            Vec<T, VE> o;
+        for (int k = 0; k < kItems; ++k) {
+            if (k * kStep >= left) continue;
+            float w[VE];
+            unpack(load_vec<V>(weight + t * VE + k * kStep), w);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) o.v[e] = from_f32<T>(h[k * VE + e]);
-            *reinterpret_cast<Vec<T, VE>*>(out + base + j) = o;
+            for (int e = 0; e < VE; ++e) h[k * VE + e] *= w[e];
         }
     }
     if (Q8) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) m = max_nan(m, fabsf(h[e]));
         const float s = max_nan(row_reduce<MaxNan, TPR>(m, part[1]) / kE4m3Max, kMinScale);
         const float inv = 1.0f / s;
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const int j = (k * TPR + t) * VE;
-            if (!live || j >= c) continue;
-            store_e4m3<VE>(q + base + j, h + k * VE, inv);
-        }
+        for (int k = 0; k < kItems; ++k)
+            if (k * kStep < left) store_e4m3<VE>(q + at + k * kStep, h + k * VE, inv);
         if (live && t == 0) scale[i] = s;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            if (k * kStep >= left) continue;
+            V o;
+            pack(h + k * VE, o);
+            store_vec(out + at + k * kStep, o);
+        }
     }
     if (rstd_out && live && t == 0) rstd_out[i] = rstd;
 }
@@ -572,7 +568,8 @@ struct NormArgs {
 template <typename T, int VE, int TPR, int E, bool Q8>
 void launch_forward_as(const NormArgs& a) {
     constexpr int kRows = Group<TPR>::kRows, kThreads = Group<TPR>::kThreads;
-    k_rms_norm<T, VE, TPR, E, Q8><<<(unsigned)((a.n + kRows - 1) / kRows), kThreads, 0, a.stream>>>(
+    const auto kernel = a.res ? k_rms_norm<T, VE, TPR, E, Q8, true> : k_rms_norm<T, VE, TPR, E, Q8, false>;
+    kernel<<<(unsigned)((a.n + kRows - 1) / kRows), kThreads, 0, a.stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.n, a.c, a.eps,
         static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
 }
