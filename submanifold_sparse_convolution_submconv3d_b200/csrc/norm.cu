@@ -71,143 +71,6 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const float* y, float inv
     }
 }
 
-// Joins v over the TPR threads of a row group of a CTA that holds several, which wait for
-// each other alone.
-template <typename Op, int TPR>
-__device__ __forceinline__ float group_reduce(float v, float* part, int group) {
-#pragma unroll
-    for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) v = Op::f(v, __shfl_xor_sync(0xffffffffu, v, d));
-    if (TPR > 32) {
-        constexpr int kWarps = TPR / 32;
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
-        const float* mine = part + group * kWarps;
-        if (kWarps <= 4) {
-            v = mine[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) v = Op::f(v, mine[w]);
-        } else {
-            const int lane = threadIdx.x & 31;
-            v = lane < kWarps ? mine[lane] : Op::id();
-#pragma unroll
-            for (int d = kWarps / 2; d > 0; d >>= 1) v = Op::f(v, __shfl_xor_sync(0xffffffffu, v, d));
-            v = __shfl_sync(0xffffffffu, v, 0);
-        }
-    }
-    return v;
-}
-
-// Rows a thread fetches ahead, in shared memory (copies of its own elements, so no thread
-// waits for another; single bf16 elements are too small to copy).
-constexpr int kAhead = 2, kStages = kAhead + 1;
-template <typename T, int VE, int E>
-constexpr bool kFetchesAhead = VE * sizeof(T) >= 4 && E * sizeof(T) <= 32;
-
-constexpr int kRingThreads = 512;
-template <typename T, int E, bool RES>
-constexpr int kForwardSmem = kStages * (RES ? 2 : 1) * E * (int)sizeof(T) * kRingThreads;
-
-// Row groups of TPR threads take one row after the other, a row in its threads' registers
-// with E elements each (item k of thread t at (k * TPR + t) * VE) and the next two rows on
-// their way into shared memory: the wait for memory and the joining of the sums, which
-// bound a group with one row, fall together with other rows' copies.
-template <typename T, int VE, int TPR, int E, bool Q8, bool RES>
-__global__ void __launch_bounds__(kRingThreads, 2)
-    k_rms_norm_ring(const T* x, const T* res, const T* __restrict__ weight, int64_t n, int c, float eps, T* sum_out,
-                    T* __restrict__ out, float* __restrict__ rstd_out, uint8_t* __restrict__ q,
-                    float* __restrict__ scale) {
-    using V = Vec<T, VE>;
-    constexpr int kRows = kRingThreads / TPR, kItems = E / VE, kBytes = VE * (int)sizeof(T);
-    extern __shared__ __align__(16) unsigned char ring_bytes[];
-    V* ring = reinterpret_cast<V*>(ring_bytes) + threadIdx.x;  // [stage][x, residual][item][thread]
-    __shared__ float red[2][2][kRingThreads / 32];
-    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    V w[kItems];
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) w[k].v[e] = from_f32<T>(1.0f);
-        const int j = (k * TPR + t) * VE;
-        if (weight && j < c) w[k] = load_vec<V>(weight + j);
-    }
-    const float by_c = 1.0f / (float)c;
-    const int64_t step = (int64_t)gridDim.x * kRows, stride = step * c;
-    int64_t i = (int64_t)blockIdx.x * kRows + group;
-    int64_t at = i * c + t * VE, at_fetch = at;  // this thread's first element of a row
-    const auto fetch = [&](bool in, int stage) {
-        V* to = ring + stage * ((RES ? 2 : 1) * kItems * kRingThreads);
-        if (in) {
-#pragma unroll
-            for (int k = 0; k < kItems; ++k) {
-                if ((k * TPR + t) * VE >= c) continue;
-                copy_async<kBytes>(shared_at(to + k * kRingThreads), x + at_fetch + k * TPR * VE);
-                if (RES) copy_async<kBytes>(shared_at(to + (kItems + k) * kRingThreads), res + at_fetch + k * TPR * VE);
-            }
-        }
-        at_fetch += stride;
-        copy_commit();
-    };
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) fetch(i + a * step < n, a);
-    int turn = 0;  // the sums' buffer: a thread may still read the last row's
-    int stage = 0;
-    for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < n; i0 += step, i += step, at += stride, turn ^= 1) {
-        const bool live = i < n;  // a group's rows join their sums together, so none leaves early
-        const V* from = ring + stage * ((RES ? 2 : 1) * kItems * kRingThreads);
-        copy_wait<kAhead - 1>();
-        float h[E], ss = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            if (!live || (k * TPR + t) * VE >= c) continue;
-            float* hk = h + k * VE;
-            unpack(from[k * kRingThreads], hk);
-            if (RES) {
-                float r[VE];
-                unpack(from[(kItems + k) * kRingThreads], r);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) hk[e] += r[e];
-                if (sum_out) {
-                    V o;
-                    pack(hk, o);
-                    store_vec(sum_out + at + k * TPR * VE, o);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < VE; ++e) ss = fmaf(hk[e], hk[e], ss);
-        }
-        fetch(i + kAhead * step < n, stage == 0 ? kStages - 1 : stage - 1);  // the stage read in the last turn
-        stage = stage == kStages - 1 ? 0 : stage + 1;
-        const float rstd = rsqrtf(group_reduce<Sum, TPR>(ss, red[turn][0], group) * by_c + eps);
-        float m = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            if (!live || (k * TPR + t) * VE >= c) continue;
-            float* y = h + k * VE;
-            float wk[VE];
-            unpack(w[k], wk);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                y[e] = y[e] * rstd * wk[e];
-                if (Q8) m = max_nan(m, fabsf(y[e]));
-            }
-            if (!Q8) {
-                V o;
-                pack(y, o);
-                store_vec(out + at + k * TPR * VE, o);
-            }
-        }
-        if (Q8) {
-            const float s = max_nan(group_reduce<MaxNan, TPR>(m, red[turn][1], group) / kE4m3Max, kMinScale);
-            const float inv = 1.0f / s;
-#pragma unroll
-            for (int k = 0; k < kItems; ++k)
-                if (live && (k * TPR + t) * VE < c) store_e4m3<VE>(q + at + k * TPR * VE, h + k * VE, inv);
-            if (live && t == 0) scale[i] = s;
-        }
-        if (rstd_out && live && t == 0) rstd_out[i] = rstd;
-    }
-}
-
 // A row lives in its threads' registers: E elements each, in items of VE, item k of
 // thread t at (k * TPR + t) * VE.  One read of x and the residual, one write of each
 // result.
@@ -338,6 +201,38 @@ inline int row_parts(int64_t n, int rows, int most) {
     return (int)(need < most ? need : most);
 }
 
+// Sum of v over the TPR threads of a row group of a CTA that holds several, which wait for
+// each other alone.
+template <int TPR>
+__device__ __forceinline__ float group_sum(float v, float* part, int group) {
+#pragma unroll
+    for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+        const float* mine = part + group * kWarps;
+        if (kWarps <= 4) {
+            v = mine[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) v += mine[w];
+        } else {
+            const int lane = threadIdx.x & 31;
+            v = lane < kWarps ? mine[lane] : 0.0f;
+#pragma unroll
+            for (int d = kWarps / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            v = __shfl_sync(0xffffffffu, v, 0);
+        }
+    }
+    return v;
+}
+
+// Rows of the gradient a thread fetches ahead, in shared memory (copies of its own elements, so no thread
+// waits for another; single bf16 elements are too small to copy).
+constexpr int kAhead = 2, kStages = kAhead + 1;
+template <typename T, int VE, int E>
+constexpr bool kFetchesAhead = VE * sizeof(T) >= 4 && E * sizeof(T) <= 32;
+
 template <typename T, int VE, int TPR, int E, bool SUM>
 constexpr int kBackwardSmem =
     kFetchesAhead<T, VE, E> ? kStages * (SUM ? 3 : 2) * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512) : 0;
@@ -432,7 +327,7 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
             fetch(i + kAhead * step < n, stage == 0 ? kStages - 1 : stage - 1);
             stage = stage == kStages - 1 ? 0 : stage + 1;
         }
-        const float mean = group_reduce<Sum, TPR>(dot, red[turn], group) * by_c;
+        const float mean = group_sum<TPR>(dot, red[turn], group) * by_c;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             if (!live || (k * TPR + t) * VE >= c) continue;
@@ -589,16 +484,6 @@ int launch_backward_sum(const NormArgs& a) {
     return parts;
 }
 
-template <typename T, int TPR, bool Q8, bool RES>
-void launch_ring_as(const NormArgs& a) {
-    constexpr int VE = 16 / (int)sizeof(T), E = 32 / (int)sizeof(T), kRows = kRingThreads / TPR, kSmem = kForwardSmem<T, E, RES>, kTurns = 12;
-    const int64_t blocks = (a.n + kRows - 1) / kRows, most = blocks / kTurns > 2 * kParts ? blocks / kTurns : 2 * kParts;
-    static std::atomic<uint64_t> done{0};
-    if (allow_smem(k_rms_norm_ring<T, VE, TPR, E, Q8, RES>, kSmem, done) != cudaSuccess) return;  // the caller asks why
-    k_rms_norm_ring<T, VE, TPR, E, Q8, RES><<<(unsigned)(blocks < most ? blocks : most), kRingThreads, kSmem, a.stream>>>(
-        static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.n, a.c, a.eps,
-        static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
-}
 // Returns the CTAs that wrote column sums.
 template <typename T, int VE, int TPR, int E>
 int launch_backward_as(const NormArgs& a) {
@@ -615,30 +500,15 @@ void launch_forward_narrow(const NormArgs& a) {
     else launch_forward_as<T, VE, 1024, 32, Q8>(a);
 }
 
-// Rows on 16-byte boundaries.  Without a residual a group has half the bytes on the way,
-// and in long rows half the warps wait for the sums: there the rows fetched ahead win
-// (200,000 x 128 bf16: 18.2 us against 24.4 a row a group; 3,000 x 8192 with residual to 8
-// bits 29.3 against 36.3).  With a residual, up to 4096 channels, one row a group does
-// (61,463 x 512 bf16: 41.4 us against 47.3), and the blocks follow each other freely.
-// A thread then holds up to 32 elements; the fewest threads that hold the row take it.
+// A thread holds up to 32 elements of a row; the fewest threads that hold it take it, so
+// that a row's sums cross few threads and the rows in work, one a group, are many.
 template <typename T, bool Q8>
 void launch_forward(const NormArgs& a) {
-    constexpr int kVe = 16 / (int)sizeof(T), kE = 32 / (int)sizeof(T);
+    constexpr int kVe = 16 / (int)sizeof(T);
     if (a.c > 32768) {
         k_rms_norm_long<T><<<(unsigned)a.n, kLongThreads, 0, a.stream>>>(
             static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.c, a.eps,
             static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
-    } else if (a.c % kVe == 0 && a.c <= 512 * kE && !a.res) {
-        if (a.c <= 4 * kE) launch_ring_as<T, 4, Q8, false>(a);
-        else if (a.c <= 8 * kE) launch_ring_as<T, 8, Q8, false>(a);
-        else if (a.c <= 16 * kE) launch_ring_as<T, 16, Q8, false>(a);
-        else if (a.c <= 32 * kE) launch_ring_as<T, 32, Q8, false>(a);
-        else if (a.c <= 64 * kE) launch_ring_as<T, 64, Q8, false>(a);
-        else if (a.c <= 128 * kE) launch_ring_as<T, 128, Q8, false>(a);
-        else if (a.c <= 256 * kE) launch_ring_as<T, 256, Q8, false>(a);
-        else launch_ring_as<T, 512, Q8, false>(a);
-    } else if (a.c % kVe == 0 && sizeof(T) == 2 && a.c > 4096 && a.c <= 512 * kE) {
-        launch_ring_as<T, 512, Q8, true>(a);
     } else if (a.c % kVe == 0) {
         if (a.c <= 64) launch_forward_as<T, kVe, 4, 16, Q8>(a);
         else if (a.c <= 128) launch_forward_as<T, kVe, 8, 16, Q8>(a);
