@@ -621,7 +621,7 @@ SPCONV_API spconv_status_t spconv_rope_free(spconv_rope_t rope);
  *             Strides in elements, in [head_dim, 2^40] (x_row is not read for n = 1,
  *             x_head not for heads = 1).  16-byte aligned buffers whose strides are
  *             multiples of 16 bytes run faster.
- *   heads     in [1, 65535].
+ *   heads     in [1, 4096].
  *   out       as x, with its own strides; rows and heads of out share no elements.
  *             May be x itself with the same strides; must not overlap it otherwise.
  *   inverse   nonzero: turn by -t.  That is also the gradient: dx from dout.
@@ -663,7 +663,9 @@ SPCONV_API spconv_status_t spconv_w4_dequantize(spconv_dtype_t dtype, const uint
  *
  * with w as above, not rounded; sums in fp32, one rounding.
  *
- *   x         device [n, cin] of dtype, or, where x_scale is given, e4m3 bytes.
+ *   x         device [n, cin] of dtype, or, where x_scale is given, e4m3 bytes.  A row
+ *             with an infinity or a NaN gives results that are not finite; finite
+ *             elements and scales are taken to stay under 2^100.
  *   x_scale   device fp32 [n] (as spconv_rms_norm_q8 writes it), or NULL.
  *   n         0 <= n <= SPCONV_W4_MAX_ROWS (more: SPCONV_ERR_UNSUPPORTED).
  *   bias      device [cout] of dtype, or NULL.

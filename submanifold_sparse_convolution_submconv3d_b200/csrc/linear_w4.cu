@@ -8,6 +8,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "row_ops.cuh"
 
 namespace spconv {
@@ -97,8 +99,8 @@ struct XShare<__nv_bfloat16, W> {
 #pragma unroll
         for (int w = 0; w < W; ++w) v[w] = in ? reinterpret_cast<const uint4*>(p)[w] : make_uint4(0, 0, 0, 0);
     }
-    __device__ uint32_t pair(int w, int i, int) const {
-        return __byte_perm(i < 2 ? v[w].x : v[w].y, i < 2 ? v[w].z : v[w].w, i & 1 ? 0x7632 : 0x5410);
+    __device__ void pair(int w, int i, uint32_t (&to)[1]) const {
+        to[0] = __byte_perm(i < 2 ? v[w].x : v[w].y, i < 2 ? v[w].z : v[w].w, i & 1 ? 0x7632 : 0x5410);
     }
 };
 template <int W>
@@ -117,7 +119,7 @@ struct XShare<__nv_fp8_e4m3, W> {
             v[0] = u.x, v[1] = u.y;
         }
     }
-    __device__ uint32_t pair(int w, int i, int) const {
+    __device__ void pair(int w, int i, uint32_t (&to)[1]) const {
         const uint32_t two = __byte_perm(v[2 * w], v[2 * w + 1], i | ((i + 4) << 4));
         uint32_t r;
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
@@ -125,7 +127,7 @@ struct XShare<__nv_fp8_e4m3, W> {
             const __half2 v16 = __hmul2(*reinterpret_cast<const __half2*>(&r), __float2half2_rn(0.0625f));
             r = *reinterpret_cast<const uint32_t*>(&v16);
         }
-        return r;
+        to[0] = r;
     }
 };
 template <int W>
@@ -139,13 +141,20 @@ struct XShare<float, W> {
             *reinterpret_cast<float4*>(v + 4 * w) =
                 in ? reinterpret_cast<const float4*>(p)[w] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    __device__ static uint32_t part_of(float x, int part) {
-        if (!(fabsf(x) <= 3.402823466e38f)) return part == 0 ? (x != x ? 0x7fc0u : __float_as_uint(x) >> 16) : 0u;
-        for (int k = 0; k < part; ++k) x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-        return __float_as_uint(x) >> 16;
+    // (an infinity has one part: what it less itself would be is no number)
+    __device__ static void split(float x, uint32_t (&part)[3]) {
+        const float most = 3.402823466e38f;
+        part[0] = __float_as_uint(x);
+        const float rest = fabsf(x) <= most ? x - __uint_as_float(part[0] & 0xffff0000u) : 0.0f;
+        part[1] = __float_as_uint(rest);
+        part[2] = __float_as_uint(rest - __uint_as_float(part[1] & 0xffff0000u));
     }
-    __device__ uint32_t pair(int w, int i, int part) const {
-        return part_of(v[8 * w + i], part) | (part_of(v[8 * w + i + 4], part) << 16);
+    __device__ void pair(int w, int i, uint32_t (&to)[3]) const {
+        uint32_t a[3], b[3];
+        split(v[8 * w + i], a);
+        split(v[8 * w + i + 4], b);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) to[p] = __byte_perm(a[p], b[p], 0x7632);  // the upper halves
     }
 };
 
@@ -155,8 +164,8 @@ struct XShare<float, W> {
 template <typename X, int NT>
 struct W4Shape {
     static constexpr int kChunk = NT == 4 || sizeof(X) == 4 ? 64 : 128;
-    static constexpr int kMostTiles = sizeof(X) == 4 ? 2 : NT == 1 ? 8 : 4;
-    static constexpr int kWarps = sizeof(X) == 4 ? 8 : NT == 1 ? 16 : 12;
+    static constexpr int kMostTiles = sizeof(X) == 4 ? 2 : 8;
+    static constexpr int kWarps = NT == 1 && sizeof(X) < 4 ? 16 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSteps = 8;  // steps (a tile of a chunk) whose codes are on the way
     static constexpr int kRingBytes = kSteps * 2 * (kChunk / 8) * kThreads;
@@ -273,25 +282,35 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
     Share raw[NT][kSubs];
     load_x(raw, warp);
 
-    // A segment's scales: on their way with the codes, in 16-byte pieces where the rows of
-    // the scales start on such a boundary.
+    // A segment's scales: on their way with the codes, in the largest pieces that the rows
+    // of the scales start on (single bf16 scales are too small to copy).
+    const auto copy_scales = [&](int seg, int held, auto bytes) {
+        constexpr int kBytes = decltype(bytes)::value, kElems = kBytes / (int)sizeof(T);
+        const int rows = min(tiles * 16, a.cout - o0), pieces = held / kElems;
+        for (int o = threadIdx.x / 16; o < rows; o += kThreads / 16) {
+            const int64_t from = (int64_t)(o0 + o) * groups + seg;
+            const uint32_t to = shared_at(table + o * kW4Pitch);
+#pragma unroll 2
+            for (int e = threadIdx.x % 16; e < pieces; e += 16) {
+                copy_async<kBytes>(to + e * kBytes, scales + from + e * kElems);
+                copy_async<kBytes>(to + kOffsets + e * kBytes, offsets + from + e * kElems);
+            }
+        }
+    };
     const auto fetch_scales = [&](int seg, int held) {
-        const int rows = min(tiles * 16, a.cout - o0);
-        const T* from[2] = {scales + (int64_t)o0 * groups + seg, offsets + (int64_t)o0 * groups + seg};
         if (groups * (int)sizeof(T) % 16 == 0) {
-            const int pieces = held * (int)sizeof(T) / 16;
-            for (int o = threadIdx.x / 16; o < rows; o += kThreads / 16)
-                for (int e = threadIdx.x % 16; e < pieces; e += 16)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-                        copy_async<16>(shared_at(table + z * kOffsets + o * kW4Pitch + e * 16),
-                                     reinterpret_cast<const unsigned char*>(from[z] + (int64_t)o * groups) + e * 16);
+            copy_scales(seg, held, std::integral_constant<int, 16>());
+        } else if (groups * (int)sizeof(T) % 4 == 0) {
+            copy_scales(seg, held, std::integral_constant<int, 4>());
         } else {
-            for (int o = threadIdx.x / 16; o < rows; o += kThreads / 16)
-                for (int k = threadIdx.x % 16; k < held; k += 16)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-                        reinterpret_cast<T*>(table + z * kOffsets + o * kW4Pitch)[k] = from[z][(int64_t)o * groups + k];
+            const int rows = min(tiles * 16, a.cout - o0);
+#pragma unroll 4
+            for (int e = threadIdx.x; e < rows * held; e += kThreads) {
+                const int o = e / held, k = e - o * held;
+                const T s = scales[(int64_t)(o0 + o) * groups + seg + k], z = offsets[(int64_t)(o0 + o) * groups + seg + k];
+                reinterpret_cast<T*>(table + o * kW4Pitch)[k] = s;
+                reinterpret_cast<T*>(table + kOffsets + o * kW4Pitch)[k] = z;
+            }
         }
     };
     int base = 0, chunk = warp;  // base: the round's first slot
@@ -311,11 +330,11 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                 for (int j = 0; j < kSubs; ++j) {
                     const uint32_t ones[4] = {C::kOne[0], C::kOne[0], C::kOne[1], C::kOne[1]};
 #pragma unroll
-                    for (int i = 0; i < kW; ++i)
+                    for (int i = 0; i < kW; ++i) {
 #pragma unroll
-                        for (int p = 0; p < kParts; ++p) {
+                        for (int e = 0; e < kOps; ++e) raw[b][j].pair(i, e, pairs[b][j][i][e]);
 #pragma unroll
-                            for (int e = 0; e < kOps; ++e) pairs[b][j][i][e][p] = raw[b][j].pair(i, e, p);
+                        for (int p = 0; p < kParts; ++p)
 #pragma unroll
                             for (int h = 0; h < kOps; h += 2) {
                                 if (i == 0 && p == 0 && h == 0)
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
                                 else
                                     mma_tile<false>(sum[b][j], ones, pairs[b][j][i][h][p], pairs[b][j][i][h + 1][p], Elem());
                             }
-                        }
+                    }
                 }
             if (chunk + kWarps < chunks) load_x(raw, chunk + kWarps);
             const int at = chunk * kChunk / GROUP - seg;  // the chunk's first group in the segment

@@ -178,7 +178,7 @@ void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cud
     const int64_t warps = (a.n + a.voxel_slots - 1) / a.voxel_slots * a.chunk_blocks;
     const int passes = (a.heads + a.head_slots - 1) / a.head_slots;
     int groups = (passes + kN - 1) / kN;
-    if (warps * groups < (int64_t)kSms * 2 * kWarps || groups * a.chunk_blocks > 65535) groups = passes;
+    if (warps * groups < (int64_t)kSms * 2 * kWarps) groups = passes;  // (times 4 blocks of items: a grid takes it)
     const int per = (passes + groups - 1) / groups;
     a.unit_heads = per * a.head_slots;
     groups = (passes + per - 1) / per;
@@ -272,7 +272,7 @@ spconv_status_t spconv_rope_apply(spconv_rope_t rope, spconv_dtype_t dtype, cons
     if (!rope) return row_fail(SPCONV_ERR_INVALID_ARG, "null handle");
     if (!dtype_ok(dtype)) return row_fail(SPCONV_ERR_INVALID_ARG, "dtype must be F32 or BF16");
     if (n < 0 || n >= (int64_t(1) << 31)) return row_fail(SPCONV_ERR_INVALID_ARG, "n must be in [0, 2^31)");
-    if (heads < 1 || heads > 65535) return row_fail(SPCONV_ERR_INVALID_ARG, "heads must be in [1, 65535]");
+    if (heads < 1 || heads > 4096) return row_fail(SPCONV_ERR_INVALID_ARG, "heads must be in [1, 4096]");
     const int64_t d = rope->head_dim, limit = int64_t(1) << 40;
     // heads and rows of one tensor must not share elements; either may be the outer one
     // (a stride over one element is not used, and taken as head_dim here)

@@ -135,7 +135,9 @@ def test_rms_norm_special_rows(sp, c, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n,c", [(1, 1), (2, 5), (3, 16), (257, 24), (1025, 128), (700, 100), (5000, 64), (33, 1024),
                                  (20, 2048), (17, 2056), (9, 4096), (3, 8192), (5, 8200), (2, 16384), (3, 20001),
-                                 (2, 32776), (1, 65536)])
+                                 (2, 32776), (1, 65536),
+                                 # several turns of every CTA
+                                 (60000, 40), (50001, 130), (6000, 515), (3000, 1001), (1700, 4096), (700, 8192), (900, 12000)])
 def test_rms_norm_backward(sp, n, c, dtype):
     for weight, dsum in ((True, False), (True, True), (False, True)):
         h, d, w = norm_inputs(n, c, dtype, dsum, weight, seed=9)
@@ -216,7 +218,9 @@ def coords_for(n, extent, seed=0):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("layout", ["interleaved", "halves"])
 @pytest.mark.parametrize("n,heads,d", [(1, 1, 2), (1, 16, 64), (2, 3, 6), (5, 2, 10), (33, 1, 64), (17, 5, 96), (64, 12, 64),
-                                       (9, 8, 128), (7, 3, 80), (3, 4, 256), (1000, 2, 32), (31, 7, 20), (3, 65, 16)])
+                                       (9, 8, 128), (7, 3, 80), (3, 4, 256), (1000, 2, 32), (31, 7, 20), (3, 65, 16), (2, 4096, 6),
+                                       # several turns of every warp
+                                       (30011, 5, 64), (20003, 12, 96), (40000, 1, 36)])
 def test_rope(sp, n, heads, d, layout, dtype):
     x = randn(n, heads, d, dtype=dtype)
     freqs, axes = ref.rope_default(d)
@@ -320,7 +324,9 @@ def x8_inputs(n, cin, seed=0):
 
 W4_SHAPES = [(32, 1, 32), (64, 8, 64), (128, 16, 128), (96, 5, 32), (160, 33, 32), (192, 64, 64), (256, 100, 64),
              (320, 129, 64), (384, 250, 128), (1024, 257, 64), (2048, 64, 128), (4096, 48, 32), (1504, 131, 32),
-             (8192, 40, 128), (4160, 1030, 64)]
+             (8192, 40, 128), (4160, 1030, 64),
+             # several tiles a CTA and waves of CTAs, ragged; more groups than a CTA holds at a time
+             (512, 9999, 64), (160, 19001, 32), (256, 40003, 128), (16416, 24, 32), (16448, 5003, 64)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -81,7 +81,7 @@ def test_rope_refusals(sp):
         return sp.lib.spconv_rope_apply(rope, dtype, coords, n, x, heads, xr, xh, out, outr, outh, 0, None)
 
     for kw in (dict(rope=None), dict(dtype=5), dict(coords=None), dict(coords=A + 4), dict(x=None), dict(out=None),
-               dict(x=B + 1), dict(out=C + 1), dict(dtype=0, x=B + 2), dict(heads=0), dict(heads=65536), dict(n=-1),
+               dict(x=B + 1), dict(out=C + 1), dict(dtype=0, x=B + 2), dict(heads=0), dict(heads=4097), dict(n=-1),
                dict(n=1 << 31), dict(xr=15), dict(xh=8), dict(outr=8), dict(outh=-16), dict(xr=1 << 41),
                dict(outr=16, outh=16),        # rows and heads of out share elements
                dict(out=B, outr=64),          # in place with other strides
