@@ -71,10 +71,11 @@ def w4_codes(packed):
 def linear_w4(x, packed, scales, offsets, bias, x_scale):
     """(out, bound on the fp32 error before the last rounding).
 
-    The sum over a group is taken on the codes less 8 (offset raised by 8 scales to
-    match), so the magnitudes are |s| |q - 8| and |z + 8 s|.  Each product is exact to
-    u; the additions form chains of at most cin / 16 + 32 steps, counted at 2 u since a
-    tensor core may cut instead of round."""
+    The sums over all groups are of the size of |s| |q - 8| + |z + 8 s| + |z|, times |x|;
+    their additions form chains of at most cin / 16 + 32 steps, counted at 2 u since a
+    tensor core may cut instead of round.  Rows of bf16 meet 128 + q within a group, which
+    the offset takes off again: at most 8 steps and 4 operations around them, at 2 u of
+    |s| (q + 128) + |128 s|, times |x|, each group."""
     q = w4_codes(packed).double()
     group = q.shape[1] // scales.shape[1]
     s, z = (t.double().repeat_interleave(group, 1) for t in (scales, offsets))
@@ -84,7 +85,10 @@ def linear_w4(x, packed, scales, offsets, bias, x_scale):
     if bias is not None:
         out = out + bias.double()
         mag = mag + bias.double().abs()
-    return out, mag * ((q.shape[1] // 16 + 32) * 2 * U)
+    err = mag * ((q.shape[1] // 16 + 32) * 2 * U)
+    if x.dtype == torch.bfloat16:
+        err = err + xs.abs() @ (s.abs() * (q + 256)).t() * (12 * 2 * U)
+    return out, err
 
 
 def w4_quantize(w, group):
