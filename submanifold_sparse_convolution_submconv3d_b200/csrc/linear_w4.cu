@@ -275,24 +275,6 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
         next += kWarps * (kChunk / 8);
         next_word += kWarps * (kChunk / 8);
     };
-#pragma unroll
-    for (int d = 0; d < kRounds; ++d) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) fetch(m, d * MT + m);
-        next_chunk();
-    }
-    const auto load_x = [&](Share (&xs)[NT][kSubs], int chunk) {
-#pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-            for (int j = 0; j < kSubs; ++j) {
-                const int row = row0 + b * 8 + g, k = chunk * kChunk + j * kSub + t * kW * 8;
-                xs[b][j].load(x + (int64_t)row * a.cin + k, row < a.n && k < a.cin);
-            }
-    };
-    Share raw[NT][kSubs];
-    load_x(raw, warp);
-
     // A segment's scales: on their way with the codes, in the largest pieces that the rows
     // of the scales start on (single bf16 scales are too small to copy).
     const auto copy_scales = [&](int seg, int held, auto bytes) {
@@ -324,13 +306,38 @@ __global__ void __launch_bounds__(W4Shape<X, NT>::kThreads)
             }
         }
     };
+    // The first scales before the first codes: the work can begin when one step is there.
+    fetch_scales(0, min(kSeg, groups));
+    copy_commit();
+#pragma unroll
+    for (int d = 0; d < kRounds; ++d) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) fetch(m, d * MT + m);
+        next_chunk();
+    }
+    const auto load_x = [&](Share (&xs)[NT][kSubs], int chunk) {
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int j = 0; j < kSubs; ++j) {
+                const int row = row0 + b * 8 + g, k = chunk * kChunk + j * kSub + t * kW * 8;
+                xs[b][j].load(x + (int64_t)row * a.cin + k, row < a.n && k < a.cin);
+            }
+    };
+    Share raw[NT][kSubs];
+    load_x(raw, warp);
+
     int base = 0, chunk = warp;  // base: the round's first slot
     for (int seg = 0; seg < groups; seg += kSeg) {
         const int held = min(kSeg, groups - seg);
-        if (seg) __syncthreads();
-        fetch_scales(seg, held);
-        copy_commit();
-        copy_wait<0>();
+        if (seg == 0) {
+            copy_wait<S::kSteps>();
+        } else {
+            __syncthreads();
+            fetch_scales(seg, held);
+            copy_commit();
+            copy_wait<0>();
+        }
         __syncthreads();
         for (; chunk < chunks && chunk * kChunk < (seg + held) * GROUP; chunk += kWarps) {
             uint32_t pairs[NT][kSubs][kW][kOps][kParts];
