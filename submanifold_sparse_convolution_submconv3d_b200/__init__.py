@@ -464,10 +464,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _elsewhere(x: torch.Tensor, stream) -> bool:
-    return stream is not None or x.get_device() != _device_now()
-
-
 @contextlib.contextmanager
 def _on(device: torch.device, stream):
     """Make ``stream`` (None: the device's current stream) the current one, so that the
@@ -516,22 +512,18 @@ def _out_like(t, like: torch.Tensor, what: str) -> torch.Tensor:
     return torch.empty_like(like) if t is None else _out(t, like, like.shape, like.dtype, what)
 
 
-def _norm_rows(x, weight, what: str) -> None:
-    if x.dtype not in _DTYPES or not x.is_cuda or x.dim() != 2:
+def _norm_rows(x, weight, what: str, more=(), names=()) -> int:
+    """Checks rows, the weight and ``more`` tensors shaped like the rows; returns the device."""
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    if dtype not in _DTYPES or index < 0 or len(shape) != 2:
         raise ValueError(f"{what} must be a float32 or bfloat16 CUDA tensor [N, C]")
-    if weight is not None:
-        _like(weight, (x.shape[1],), x.dtype, x.device, "weight")
-
-
-def _norm_inputs(x, weight, residual, sum_out) -> tuple:
-    if residual is not None:
-        _like(residual, x.shape, x.dtype, x.device, "residual")
-        residual = _in(residual)
-    elif sum_out is not None:
-        raise ValueError("sum_out needs a residual")
-    x = _in(x)
-    return (x, None if weight is None else _in(weight), residual,
-            None if residual is None else _out_like(sum_out, x, "sum_out"))
+    if weight is not None and (weight.dtype is not dtype or weight.get_device() != index or weight.dim() != 1
+                               or weight.numel() != shape[1]):
+        _like(weight, shape[1:], dtype, x.device, "weight")
+    for t, name in zip(more, names):
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+            _like(t, shape, dtype, x.device, name)
+    return index
 
 
 def spconv_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
@@ -542,17 +534,23 @@ def spconv_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residua
     ``sum_out`` may be ``residual`` or ``x`` itself; ``rstd``, a float32 CUDA tensor [N],
     receives what ``spconv_rms_norm_backward`` reads."""
     _require()
-    _norm_rows(x, weight, "x")
-    if _elsewhere(x, stream):
+    index = _norm_rows(x, weight, "x", () if residual is None else (residual,), ("residual",))
+    if stream is not None or index != _device_now():
         with _on(x.device, stream):
             return spconv_rms_norm(x, weight, residual, eps, out, sum_out, rstd)
     n, c = x.shape
-    x, weight, residual, sum_out = _norm_inputs(x, weight, residual, sum_out)
+    x = _in(x)
+    if weight is not None:
+        weight = _in(weight)
+    if residual is not None:
+        residual, sum_out = _in(residual), _out_like(sum_out, x, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
     if rstd is not None:
         _out(rstd, x, (n,), torch.float32, "rstd")
     out = _out_like(out, x, "out")
-    _check(lib.spconv_rms_norm(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), n, c, eps,
-                               _ptr(sum_out), out.data_ptr(), _ptr(rstd), _raw_stream(x.get_device())))
+    _check(lib.spconv_rms_norm(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), n, c, eps, _ptr(sum_out),
+                               out.data_ptr(), _ptr(rstd), _raw_stream(index)))
     return out if residual is None else (out, sum_out)
 
 
@@ -563,16 +561,23 @@ def spconv_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, resi
     scale, sum)``, q float8_e4m3fn [N, C] and scale float32 [N], the norm being about
     q * scale."""
     _require()
-    _norm_rows(x, weight, "x")
-    if _elsewhere(x, stream):
+    index = _norm_rows(x, weight, "x", () if residual is None else (residual,), ("residual",))
+    if stream is not None or index != _device_now():
         with _on(x.device, stream):
             return spconv_rms_norm_q8(x, weight, residual, eps, out, scale, sum_out)
     n, c = x.shape
-    x, weight, residual, sum_out = _norm_inputs(x, weight, residual, sum_out)
-    out = _out(out, x, (n, c), torch.float8_e4m3fn, "out")
+    x = _in(x)
+    if weight is not None:
+        weight = _in(weight)
+    if residual is not None:
+        residual, sum_out = _in(residual), _out_like(sum_out, x, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    out = torch.empty_like(x, dtype=torch.float8_e4m3fn) if out is None else \
+        _out(out, x, (n, c), torch.float8_e4m3fn, "out")
     scale = _out(scale, x, (n,), torch.float32, "scale")
     _check(lib.spconv_rms_norm_q8(_DTYPES[x.dtype], x.data_ptr(), _ptr(residual), _ptr(weight), n, c, eps,
-                                  _ptr(sum_out), out.data_ptr(), scale.data_ptr(), _raw_stream(x.get_device())))
+                                  _ptr(sum_out), out.data_ptr(), scale.data_ptr(), _raw_stream(index)))
     return (out, scale) if residual is None else (out, scale, sum_out)
 
 
@@ -591,17 +596,16 @@ def spconv_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
     ``dsum``, the gradient that reaches the sum by other ways, added (dx may be dsum
     itself).  dweight is float32 [C], or None without a weight or with weight_grad False."""
     _require()
-    _norm_rows(h, weight, "h")
-    if _elsewhere(h, stream):
+    index = _norm_rows(h, weight, "h", (dy,) if dsum is None else (dy, dsum), ("dy", "dsum"))
+    if stream is not None or index != _device_now():
         with _on(h.device, stream):
             return spconv_rms_norm_backward(dy, h, weight, rstd, dsum, dx, weight_grad)
     n, c = h.shape
-    _like(dy, h.shape, h.dtype, h.device, "dy")
-    _like(rstd, (n,), torch.float32, h.device, "rstd")
-    if dsum is not None:
-        _like(dsum, h.shape, h.dtype, h.device, "dsum")
-        dsum = _in(dsum)
+    if rstd.dim() != 1 or rstd.numel() != n or rstd.dtype is not torch.float32 or rstd.get_device() != index:
+        _like(rstd, (n,), torch.float32, h.device, "rstd")
     dy, h, rstd = _in(dy), _in(h), _in(rstd)
+    if dsum is not None:
+        dsum = _in(dsum)
     dx = _out_like(dx, h, "dx")
     dweight = workspace = None
     if weight is not None:
@@ -611,7 +615,7 @@ def spconv_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Te
             dweight = rstd.new_empty(c)
     _check(lib.spconv_rms_norm_backward(_DTYPES[h.dtype], dy.data_ptr(), h.data_ptr(), _ptr(weight), rstd.data_ptr(),
                                         _ptr(dsum), n, c, dx.data_ptr(), _ptr(dweight), _ptr(workspace),
-                                        _raw_stream(h.get_device())))
+                                        _raw_stream(index)))
     return dx, dweight
 
 
@@ -671,40 +675,45 @@ def spconv_rope_apply(rope: Rope, coords: torch.Tensor, x: torch.Tensor, out: to
     _require()
     if not rope.handle:
         raise ValueError("the rope has been freed")
-    if x.dtype not in _DTYPES or not x.is_cuda or x.dim() != 3 or x.shape[2] != rope.head_dim or x.shape[1] < 1:
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    if dtype not in _DTYPES or index < 0 or len(shape) != 3 or shape[2] != rope.head_dim or shape[1] < 1:
         raise ValueError(f"x must be a float32 or bfloat16 CUDA tensor [N, heads, {rope.head_dim}]")
-    if coords.dtype != torch.int32 or coords.shape != (x.shape[0], 4) or coords.device != x.device:
-        raise ValueError(f"coords must be an int32 tensor [{x.shape[0]}, 4] on {x.device}")
-    if _elsewhere(x, stream):
+    n, heads, d = shape
+    if coords.dtype is not torch.int32 or coords.shape != (n, 4) or coords.get_device() != index:
+        raise ValueError(f"coords must be an int32 tensor [{n}, 4] on {x.device}")
+    if stream is not None or index != _device_now():
         with _on(x.device, stream):
             return spconv_rope_apply(rope, coords, x, out, inverse)
-    n, heads, d = x.shape
+    row, head, one = x.stride()
     if out is None:
-        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty((n, heads, d))
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
     else:
-        _like(out, x.shape, x.dtype, x.device, "out")
+        _like(out, shape, dtype, x.device, "out")
         if out.stride(2) != 1:
             raise ValueError("the heads of out must be contiguous")
-    if x.stride(2) != 1 or (n > 1 and x.stride(0) < d) or (heads > 1 and x.stride(1) < d):
+    if one != 1 or (n > 1 and row < d) or (heads > 1 and head < d):
         x = x.contiguous()
+        row, head, one = x.stride()
     coords = _in(coords)
-    _check(lib.spconv_rope_apply(rope.handle, _DTYPES[x.dtype], coords.data_ptr(), n, x.data_ptr(), heads, x.stride(0),
-                                 x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), bool(inverse),
-                                 _raw_stream(x.get_device())))
+    out_row, out_head, one = out.stride()
+    _check(lib.spconv_rope_apply(rope.handle, _DTYPES[dtype], coords.data_ptr(), n, x.data_ptr(), heads, row, head,
+                                 out.data_ptr(), out_row, out_head, bool(inverse), _raw_stream(index)))
     return out
 
 
-def _w4_args(packed, scales, offsets) -> tuple[int, int, int]:
-    """(cin, cout, group) of 4-bit weights."""
-    if scales.dtype not in _DTYPES or not scales.is_cuda or scales.dim() != 2:
+def _w4_args(packed, scales, offsets) -> tuple[int, int, int, int]:
+    """(cin, cout, group, device) of 4-bit weights."""
+    shape, codes, dtype, index = scales.shape, packed.shape, scales.dtype, scales.get_device()
+    if dtype not in _DTYPES or index < 0 or len(shape) != 2:
         raise ValueError("scales must be a float32 or bfloat16 CUDA tensor [Cout, Cin / group]")
-    _like(offsets, scales.shape, scales.dtype, scales.device, "offsets")
-    if packed.dtype != torch.int32 or packed.device != scales.device or packed.dim() != 2 \
-            or packed.shape[0] != scales.shape[0] or scales.shape[1] < 1 or packed.shape[1] * 8 % scales.shape[1]:
+    if offsets.shape != shape or offsets.dtype is not dtype or offsets.get_device() != index:
+        _like(offsets, shape, dtype, scales.device, "offsets")
+    if packed.dtype is not torch.int32 or packed.get_device() != index or len(codes) != 2 or codes[0] != shape[0] \
+            or shape[1] < 1 or codes[1] * 8 % shape[1]:
         raise ValueError(f"packed must be an int32 tensor [Cout, Cin / 8] on {scales.device}, with scales "
-                         f"[Cout, Cin / group]; got {list(packed.shape)} and {list(scales.shape)}")
-    cin = packed.shape[1] * 8
-    return cin, packed.shape[0], cin // scales.shape[1]
+                         f"[Cout, Cin / group]; got {list(codes)} and {list(shape)}")
+    cin = codes[1] * 8
+    return cin, codes[0], cin // shape[1], index
 
 
 def spconv_w4_quantize(w: torch.Tensor, group: int = 64, stream=None) -> tuple:
@@ -718,7 +727,7 @@ def spconv_w4_quantize(w: torch.Tensor, group: int = 64, stream=None) -> tuple:
     cin, cout = w.shape
     if group not in (32, 64, 128) or cin < group or cin % group or cout < 1:
         raise ValueError(f"group must be 32, 64 or 128 and divide Cin = {cin}; Cout must be at least 1")
-    if _elsewhere(w, stream):
+    if stream is not None or w.get_device() != _device_now():
         with _on(w.device, stream):
             return spconv_w4_quantize(w, group)
     w = _in(w)
@@ -734,8 +743,8 @@ def spconv_w4_dequantize(packed: torch.Tensor, scales: torch.Tensor, offsets: to
     """The weights back, [1, Cin, Cout] of the scales' dtype: the weights of a layer of
     kernel size 1, for more rows than ``spconv_linear_w4`` takes."""
     _require()
-    cin, cout, group = _w4_args(packed, scales, offsets)
-    if _elsewhere(scales, stream):
+    cin, cout, group, index = _w4_args(packed, scales, offsets)
+    if stream is not None or index != _device_now():
         with _on(scales.device, stream):
             return spconv_w4_dequantize(packed, scales, offsets, out)
     out = _out(out, scales, (1, cin, cout), scales.dtype, "out")
@@ -752,23 +761,25 @@ def spconv_linear_w4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor
     scales' dtype, or float8_e4m3fn with ``x_scale`` float32 [N] (as
     ``spconv_rms_norm_q8`` returns them) -> out [N, Cout] of the scales' dtype."""
     _require()
-    cin, cout, group = _w4_args(packed, scales, offsets)
-    dtype, device, n = scales.dtype, scales.device, x.shape[0] if x.dim() else 0
-    _like(x, (n, cin), dtype if x_scale is None else torch.float8_e4m3fn, device, "x")
-    if _elsewhere(scales, stream):
-        with _on(device, stream):
+    cin, cout, group, index = _w4_args(packed, scales, offsets)
+    dtype, n = scales.dtype, x.shape[0] if x.dim() else 0
+    if x.shape != (n, cin) or x.dtype is not (dtype if x_scale is None else torch.float8_e4m3fn) \
+            or x.get_device() != index:
+        _like(x, (n, cin), dtype if x_scale is None else torch.float8_e4m3fn, scales.device, "x")
+    if stream is not None or index != _device_now():
+        with _on(scales.device, stream):
             return spconv_linear_w4(x, packed, scales, offsets, bias, x_scale, out)
     if x_scale is not None:
-        _like(x_scale, (n,), torch.float32, device, "x_scale")
+        _like(x_scale, (n,), torch.float32, scales.device, "x_scale")
         x_scale = _in(x_scale)
     if bias is not None:
-        _like(bias, (cout,), dtype, device, "bias")
+        _like(bias, (cout,), dtype, scales.device, "bias")
         bias = _in(bias)
-    out = _out(out, scales, (n, cout), dtype, "out")
+    out = scales.new_empty((n, cout)) if out is None else _out(out, scales, (n, cout), dtype, "out")
     x, packed, scales, offsets = _in(x), _in(packed), _in(scales), _in(offsets)
     _check(lib.spconv_linear_w4(_DTYPES[dtype], x.data_ptr(), _ptr(x_scale), n, cin, packed.data_ptr(),
                                 scales.data_ptr(), offsets.data_ptr(), group, _ptr(bias), out.data_ptr(), cout,
-                                _raw_stream(scales.get_device())))
+                                _raw_stream(index)))
     return out
 
 
