@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kLongThreads)
 
 // CTAs that share the rows of the gradient: a constant, so that the order of the column
 // sums depends on the shape alone.  One CTA of 512 threads an SM; more of them add column
-// sums to join (8,191 x 4096 bf16: 40.4 us with 148 CTAs, 42.8 with 296).  Rows that are
-// not fetched ahead run on two, which cover each other's waits.
+// sums to join (8,191 x 4096 bf16: 40.4 us with 148 CTAs, 42.8 with 296).  The longest
+// rows, which are read twice, run on two, which cover each other's waits.
 constexpr int kParts = kSms, kMaxParts = 2 * kParts;
 inline int row_parts(int64_t n, int rows, int most) {
     // Up to four turns of one CTA: its column sums are the result, and the second step's
@@ -231,36 +231,88 @@ __device__ __forceinline__ float group_sum(float v, float* part, int group) {
     return v;
 }
 
-// Rows of the gradient a thread fetches ahead, in shared memory (copies of its own elements, so no thread
-// waits for another; single bf16 elements are too small to copy).
-constexpr int kAhead = 2, kStages = kAhead + 1;
-template <typename T, int VE, int E>
-constexpr bool kFetchesAhead = VE * sizeof(T) >= 4 && E * sizeof(T) <= 32;
+// Rows of the gradient a thread fetches ahead, in shared memory: copies of its own elements,
+// so no thread waits for another.
+template <typename T, int TPR, int E, bool SUM>  // two rows ahead of the one in work, or one
+constexpr int kRowSmem = (SUM ? 3 : 2) * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512);
+template <typename T, int TPR, int E, bool SUM>
+constexpr int kAhead = 3 * kRowSmem<T, TPR, E, SUM> <= 200 * 1024 ? 2 : 1;
+template <typename T, int TPR, int E>
+constexpr bool kFetchesAhead = E <= 16 && 2 * kRowSmem<T, TPR, E, true> <= 200 * 1024;
 
-template <typename T, int VE, int TPR, int E, bool SUM>
+// Dynamic shared memory: the rows on their way, and at the end the column sums of a CTA that
+// has one row at a time (with a place left free after every 32).
+template <typename T, int TPR, int E, bool SUM>
+constexpr int kRingSmem =
+    kFetchesAhead<T, TPR, E> ? (kAhead<T, TPR, E, SUM> + 1) * kRowSmem<T, TPR, E, SUM> : 0;
+template <typename T, int TPR, int E, bool SUM>
 constexpr int kBackwardSmem =
-    kFetchesAhead<T, VE, E> ? kStages * (SUM ? 3 : 2) * E * (int)sizeof(T) * (TPR > 512 ? TPR : 512) : 0;
+    TPR >= 512 && kRingSmem<T, TPR, E, SUM> < TPR * E / 32 * 33 * 4 ? TPR * E / 32 * 33 * 4 : kRingSmem<T, TPR, E, SUM>;
+
+// Elements [from, to) of an item of 16 bytes, which are not all of it.
+__device__ __forceinline__ void store_part(float* p, const Vec<float, 4>& v, int from, int to) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e >= from && e < to) p[e] = v.v[e];
+}
+__device__ __forceinline__ void store_part(__nv_bfloat16* p, const Vec<__nv_bfloat16, 8>& v, int from, int to) {
+    uint32_t w[4];
+    memcpy(w, &v, 16);
+    if (from > 0 && to < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e >= from && e < to) p[e] = v.v[e];
+    } else if (from > 0) {  // up to a whole word, then two words, then four
+        const int word = (from + 1) >> 1;
+        const uint32_t first = from >= 4 ? from >= 6 ? w[3] : w[2] : from >= 2 ? w[1] : w[0];
+        if (from & 1) reinterpret_cast<uint16_t*>(p)[from] = (uint16_t)(first >> 16);
+        if (word & 1) reinterpret_cast<uint32_t*>(p)[word] = word == 1 ? w[1] : w[3];
+        if (word <= 2) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
+    } else {
+        const uint32_t last = to >= 4 ? to >= 6 ? w[3] : w[2] : to >= 2 ? w[1] : w[0];
+        if (to & 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        if (to & 2) reinterpret_cast<uint32_t*>(p)[to >= 4 ? 2 : 0] = to >= 4 ? w[2] : w[0];
+        if (to & 1) reinterpret_cast<uint16_t*>(p)[to - 1] = (uint16_t)last;
+    }
+}
 
 // dx of the rows and, in `part`, each CTA's column sums of dy * xh.  A CTA's row groups
 // of TPR threads take rows blockIdx.x * kRows + group, and so on by gridDim.x * kRows,
 // and wait only within the group; a thread keeps the sums of its columns in registers
 // over all its rows, and the groups' sums are joined in shared memory at the end.
+//
+// SHIFT: rows of c elements where c is no multiple of an item's VE.  The grid makes a group's
+// turns a multiple of VE elements apart, so each of its rows starts `shift` elements behind an
+// item's start: the items are read whole, the elements of the row before are taken as zero,
+// those behind the row are not read, and the two ends are written by elements.  Against rows
+// read by one or two elements: 220,147 x 53 bf16 with a dsum 26.5 us, was 77; 24,198 x 379
+// 23.2, was 77; 2,214 x 5491 24.1, was 527 (it did not fit the registers).
+//
 // Memory bounds it as long as the next rows are on their way: without them (loads at
 // the top of a turn) 8,191 x 4096 bf16 take 66 us, with them 37.0 us, 5.4 TB/s or 83 % of a
-// copy's rate with the sums' second step in it; 209,715 x 128 with a dsum 37.5 us (88 %).
-template <typename T, int VE, int TPR, int E, bool SUM>
-__global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 && !kFetchesAhead<T, VE, E> ? 2 : 1)
+// copy's rate with the sums' second step in it; 209,715 x 128 with a dsum 37.5 us (88 %),
+// 3,000 x 6000 fp32 38.6 us (85 %).
+template <typename T, int VE, int TPR, int E, bool SUM, bool SHIFT>
+__global__ void __launch_bounds__(TPR > 512 ? TPR : 512)
     k_rms_norm_backward(const T* __restrict__ dy, const T* __restrict__ h, const T* __restrict__ weight,
                         const float* __restrict__ rstd_in, const T* dsum, int64_t n, int c, T* dx,
                         float* __restrict__ part) {
     using V = Vec<T, VE>;
     constexpr int kThreads = TPR > 512 ? TPR : 512, kRows = kThreads / TPR, kItems = E / VE;
-    constexpr bool kFetch = kFetchesAhead<T, VE, E>;
-    constexpr int kBytes = VE * sizeof(T) < 4 ? 4 : VE * (int)sizeof(T);  // (not copied under 4)
+    constexpr bool kFetch = kFetchesAhead<T, TPR, E>;
+    constexpr int kTurns = kAhead<T, TPR, E, SUM>, kStages = kTurns + 1;
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     V* ring = reinterpret_cast<V*>(ring_bytes) + threadIdx.x;  // [stage][dy, h, dsum][item][thread]
     __shared__ float red[2][kThreads / 32];
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    // With a shift the rows of a warp lie 16 apart, so that they all have the same one.
+    const int row = SHIFT && TPR < 32 ? threadIdx.x % 32 / TPR * (kThreads / 32) + threadIdx.x / 32 : group;
+    const int64_t step = (int64_t)gridDim.x * kRows, stride = step * c;
+    int64_t i = (int64_t)blockIdx.x * kRows + row;
+    const int shift = SHIFT ? (int)(i * c) & (VE - 1) : 0, end = c + shift;
+    const int head = t == 0 ? shift : 0;  // this many elements of item 0 belong to the row before
+    const bool edge = head > 0 || (end % VE > 0 && end / VE % TPR == t);  // has an item with some of the row
+    int64_t at = i * c - shift + t * VE, at_fetch = at;  // this thread's first element of a row
     float dw[E];
     V w[kItems];
 #pragma unroll
@@ -270,22 +322,33 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
         const int j = (k * TPR + t) * VE;
 #pragma unroll
         for (int e = 0; e < VE; ++e) w[k].v[e] = from_f32<T>(1.0f);
-        if (weight && j < c) w[k] = load_vec<V>(weight + j);
+        if (SHIFT) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (weight && j + e >= shift && j + e < end) w[k].v[e] = weight[j + e - shift];
+        } else if (weight && j < c) {
+            w[k] = load_vec<V>(weight + j);
+        }
     }
     const float by_c = 1.0f / (float)c;
-    const int64_t step = (int64_t)gridDim.x * kRows, stride = step * c;
-    int64_t i = (int64_t)blockIdx.x * kRows + group;
-    int64_t at = i * c + t * VE, at_fetch = at;  // this thread's first element of a row
     const auto fetch = [&](bool in, int stage) {
         V* to = ring + stage * ((SUM ? 3 : 2) * kItems * kThreads);
         if (in) {
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
-                if ((k * TPR + t) * VE >= c) continue;
+                const int j = (k * TPR + t) * VE;
+                if (j >= end) continue;
                 const int64_t from = at_fetch + k * TPR * VE;
-                copy_async<kBytes>(shared_at(to + k * kThreads), dy + from);
-                copy_async<kBytes>(shared_at(to + (kItems + k) * kThreads), h + from);
-                if (SUM) copy_async<kBytes>(shared_at(to + (2 * kItems + k) * kThreads), dsum + from);
+                const auto copy = [&](int array, const T* src) {
+                    const uint32_t dst = shared_at(to + (array * kItems + k) * kThreads);
+                    // an item is read as far as the row goes; the rest of it is zero
+                    if (SHIFT)
+                        copy_async_part(dst, src + from, (end - j < VE ? end - j : VE) * (int)sizeof(T));
+                    else
+                        copy_async<16>(dst, src + from);
+                };
+                copy(0, dy), copy(1, h);
+                if (SUM) copy(2, dsum);
             }
         }
         at_fetch += stride;
@@ -293,7 +356,7 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
     };
     if (kFetch) {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) fetch(i + a * step < n, a);
+        for (int a = 0; a < kTurns; ++a) fetch(i + a * step < n, a);
     }
     float rstd_next = i < n ? rstd_in[i] : 0.0f;
     int turn = 0;  // the sums' buffer: a thread may still read the last row's
@@ -304,10 +367,21 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
         rstd_next = i + step < n ? rstd_in[i + step] : 0.0f;
         V vd[kItems], vh[kItems], vs[kItems];
         const V* from = ring + stage * ((SUM ? 3 : 2) * kItems * kThreads);
-        if (kFetch) copy_wait<kAhead - 1>();
+        if (kFetch) copy_wait<kTurns - 1>();
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            if (!live || (k * TPR + t) * VE >= c) continue;
+            const int j = (k * TPR + t) * VE;
+            if (!live || j >= end) continue;
+            if (SHIFT && !kFetch && j + VE > end) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const bool in = j + e < end;
+                    vd[k].v[e] = in ? dy[at + k * TPR * VE + e] : from_f32<T>(0.0f);
+                    vh[k].v[e] = in ? h[at + k * TPR * VE + e] : from_f32<T>(0.0f);
+                    if (SUM) vs[k].v[e] = in ? dsum[at + k * TPR * VE + e] : from_f32<T>(0.0f);
+                }
+                continue;
+            }
             vd[k] = kFetch ? from[k * kThreads] : load_vec<V>(dy + at + k * TPR * VE);
             vh[k] = kFetch ? from[(kItems + k) * kThreads] : load_vec<V>(h + at + k * TPR * VE);
             if (SUM) vs[k] = kFetch ? from[(2 * kItems + k) * kThreads] : load_vec<V>(dsum + at + k * TPR * VE);
@@ -315,7 +389,7 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
         float g[E], xh[E], dot = 0.0f;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            if (!live || (k * TPR + t) * VE >= c) continue;
+            if (!live || (k * TPR + t) * VE >= end) continue;
             float d[VE], wk[VE];
             unpack(vd[k], d);
             unpack(vh[k], xh + k * VE);
@@ -323,6 +397,7 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 const int o = k * VE + e;
+                if (SHIFT && k == 0 && e < head) d[e] = xh[o] = 0.0f;
                 xh[o] *= rstd;
                 g[o] = d[e] * wk[e];
                 dw[o] = fmaf(d[e], xh[o], dw[o]);
@@ -331,13 +406,14 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
         }
         if (kFetch) {
             // into the stage read in the last turn
-            fetch(i + kAhead * step < n, stage == 0 ? kStages - 1 : stage - 1);
+            fetch(i + kTurns * step < n, stage == 0 ? kStages - 1 : stage - 1);
             stage = stage == kStages - 1 ? 0 : stage + 1;
         }
         const float mean = group_sum<TPR>(dot, red[turn], group) * by_c;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            if (!live || (k * TPR + t) * VE >= c) continue;
+            const int j = (k * TPR + t) * VE;
+            if (!live || j >= end) continue;
             float o[VE], ds[VE];
             if (SUM) unpack(vs[k], ds);
 #pragma unroll
@@ -345,22 +421,41 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
                 o[e] = fmaf(-xh[k * VE + e], mean, g[k * VE + e]);
                 o[e] = SUM ? fmaf(rstd, o[e], ds[e]) : rstd * o[e];
             }
-            V packed;
-            pack(o, packed);
-            store_vec(dx + at + k * TPR * VE, packed);
+            if constexpr (SHIFT) {
+                pack(o, vd[k]);
+                if (j >= shift && j + VE <= end) store_vec(dx + at + k * TPR * VE, vd[k]);
+            } else {
+                V packed;
+                pack(o, packed);
+                store_vec(dx + at + k * TPR * VE, packed);
+            }
+        }
+        if (SHIFT && edge && live) {
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int j = (k * TPR + t) * VE;
+                if (j < end && (j < shift || j + VE > end))
+                    store_part(dx + at + k * TPR * VE, vd[k], k == 0 ? head : 0, end - j < VE ? end - j : VE);
+            }
         }
     }
     cudaTriggerProgrammaticLaunchCompletion();  // the column sums' second step may take its place
     if (!part) return;
     part += (int64_t)blockIdx.x * c;
     if constexpr (kRows == 1) {
+        // from a thread's neighbouring columns to neighbouring threads' (written from the
+        // registers, 148 x 6688 sums take 8 us)
+        __syncthreads();  // the rows' place is free
+        float* cols = reinterpret_cast<float*>(ring_bytes);
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const int j = (k * TPR + t) * VE;
-            if (j >= c) continue;
+        for (int k = 0; k < kItems; ++k)
 #pragma unroll
-            for (int e = 0; e < VE; ++e) part[j + e] = dw[k * VE + e];
-        }
+            for (int e = 0; e < VE; ++e) {
+                const int j = (k * TPR + t) * VE + e - shift;
+                if (!SHIFT || j >= 0) cols[j + (j >> 5)] = dw[k * VE + e];
+            }
+        __syncthreads();
+        for (int j = threadIdx.x; j < c; j += kThreads) part[j] = cols[j + (j >> 5)];
     } else {
         // a warp's groups first (TPR < 32), then the groups: kShares rows of sums
         constexpr int kShares = TPR < 32 ? kThreads / 32 : kRows;
@@ -373,8 +468,10 @@ __global__ void __launch_bounds__(TPR > 512 ? TPR : 512, TPR <= 512 && E <= 16 &
 #pragma unroll
             for (int k = 0; k < kItems; ++k)
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    cols[TPR < 32 ? threadIdx.x / 32 : group][(k * TPR + t) * VE + e] = dw[k * VE + e];
+                for (int e = 0; e < VE; ++e) {
+                    const int j = (k * TPR + t) * VE + e - shift;
+                    if (!SHIFT || j >= 0) cols[TPR < 32 ? threadIdx.x / 32 : group][j] = dw[k * VE + e];
+                }
         }
         __syncthreads();
         for (int j = threadIdx.x; j < c; j += kThreads) {
@@ -476,34 +573,21 @@ void launch_forward_as(const NormArgs& a) {
         static_cast<T*>(a.sum_out), static_cast<T*>(a.out), a.rstd, a.q, a.scale);
 }
 
-template <typename T, int VE, int TPR, int E, bool SUM>
-int launch_backward_sum(const NormArgs& a) {
-    constexpr int kThreads = TPR > 512 ? TPR : 512, kSmem = kBackwardSmem<T, VE, TPR, E, SUM>;
-    const int parts = row_parts(a.n, kThreads / TPR, kFetchesAhead<T, VE, E> ? kParts : kMaxParts);
-    float* part = parts == 1 ? a.dweight : a.part;
-    if (kSmem > 0) {
-        static std::atomic<uint64_t> done{0};
-        if (allow_smem(k_rms_norm_backward<T, VE, TPR, E, SUM>, kSmem, done) != cudaSuccess) return 0;  // the caller asks why
-    }
-    k_rms_norm_backward<T, VE, TPR, E, SUM><<<parts, kThreads, kSmem, a.stream>>>(
-        static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
-        static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), part);
-    return parts;
-}
-
-// Returns the CTAs that wrote column sums.
-template <typename T, int VE, int TPR, int E>
-int launch_backward_as(const NormArgs& a) {
-    return a.dsum ? launch_backward_sum<T, VE, TPR, E, true>(a) : launch_backward_sum<T, VE, TPR, E, false>(a);
-}
-
-// Rows that do not start on 16-byte boundaries: two elements at a time, or one.
+// Rows that do not start on 16-byte boundaries: two elements at a time, or one.  Up to 1024
+// channels a warp takes the row (61,463 x 513 bf16: 37 us; 46 with 128 threads a row, which
+// wait for each other), longer rows have 16 to 32 elements a thread.
 template <typename T, int VE, bool Q8>
 void launch_forward_narrow(const NormArgs& a) {
-    if (a.c <= 256) launch_forward_as<T, VE, 16, 16, Q8>(a);
+    if (a.c <= 32) launch_forward_as<T, VE, 4, 8, Q8>(a);
+    else if (a.c <= 64) launch_forward_as<T, VE, 4, 16, Q8>(a);
+    else if (a.c <= 128) launch_forward_as<T, VE, 16, 8, Q8>(a);
+    else if (a.c <= 256) launch_forward_as<T, VE, 32, 8, Q8>(a);
     else if (a.c <= 512) launch_forward_as<T, VE, 32, 16, Q8>(a);
-    else if (a.c <= 1024) launch_forward_as<T, VE, 128, 8, Q8>(a);
-    else if (a.c <= 4096) launch_forward_as<T, VE, 512, 8, Q8>(a);
+    else if (a.c <= 1024) launch_forward_as<T, VE, 32, 32, Q8>(a);
+    else if (a.c <= 2048) launch_forward_as<T, VE, 128, 16, Q8>(a);
+    else if (a.c <= 4096) launch_forward_as<T, VE, 256, 16, Q8>(a);
+    else if (a.c <= 8192) launch_forward_as<T, VE, 256, 32, Q8>(a);
+    else if (a.c <= 16384) launch_forward_as<T, VE, 512, 32, Q8>(a);
     else launch_forward_as<T, VE, 1024, 32, Q8>(a);
 }
 
@@ -534,41 +618,67 @@ void launch_forward(const NormArgs& a) {
     }
 }
 
-template <typename T, int VE>
-int launch_backward_narrow(const NormArgs& a) {
-    constexpr int kE = VE * sizeof(T) < 4 ? 8 : 32 / (int)sizeof(T);  // single bf16: nothing on the way
-    if (a.c <= 16 * kE) return launch_backward_as<T, VE, 16, kE>(a);
-    if (a.c <= 32 * kE) return launch_backward_as<T, VE, 32, kE>(a);
-    if (a.c <= 128 * kE) return launch_backward_as<T, VE, 128, kE>(a);
-    if (a.c <= 512 * kE) return launch_backward_as<T, VE, 512, kE>(a);
-    return launch_backward_as<T, VE, 1024, 32>(a);
+template <typename T, int TPR, int E, bool SUM, bool SHIFT>
+int launch_backward_kernel(const NormArgs& a) {
+    constexpr int kThreads = TPR > 512 ? TPR : 512, kRows = kThreads / TPR, kVe = 16 / (int)sizeof(T);
+    constexpr int kSmem = kBackwardSmem<T, TPR, E, SUM>;
+    constexpr auto kernel = k_rms_norm_backward<T, kVe, TPR, E, SUM, SHIFT>;
+    int parts = row_parts(a.n, kRows, kParts);
+    if (SHIFT && (int64_t)parts * kRows < a.n) {
+        // A group keeps its shift over its turns: they are a whole number of items apart.
+        int whole = 1;
+        while ((int64_t)whole * kRows * a.c % kVe) whole *= 2;
+        if (parts % whole) parts = parts == 1 ? (int)((a.n + kRows - 1) / kRows) : parts / whole * whole;
+    }
+    if (kSmem > 0) {
+        static std::atomic<uint64_t> done{0};
+        if (allow_smem(kernel, kSmem, done) != cudaSuccess) return 0;  // the caller asks why
+    }
+    kernel<<<parts, kThreads, kSmem, a.stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
+        static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), parts == 1 ? a.dweight : a.part);
+    return parts;
 }
 
-// 32 bytes of a row a thread (bf16: 16 elements, fp32: 8), then more.
+// Returns the CTAs that wrote column sums.
+template <typename T, int TPR, int E>
+int launch_backward_as(const NormArgs& a) {
+    if (a.c % (16 / (int)sizeof(T)) == 0)
+        return a.dsum ? launch_backward_kernel<T, TPR, E, true, false>(a) : launch_backward_kernel<T, TPR, E, false, false>(a);
+    return a.dsum ? launch_backward_kernel<T, TPR, E, true, true>(a) : launch_backward_kernel<T, TPR, E, false, true>(a);
+}
+
+// A row's items from its first element's: a row that does not start at one may touch one more.
+template <typename T>
+int row_span(int c) {
+    constexpr int kVe = 16 / (int)sizeof(T);
+    return c % kVe == 0 ? c : c + kVe - 1;
+}
+
+// 32 bytes of a row a thread (bf16: 16 elements, fp32: 8), as many threads as that takes; 16
+// bytes a thread and twice the threads are a quarter to a half slower.  From 16,384 channels on
+// the columns' sums do not fit the registers: 900 x 20,000 bf16 take 97 us with 32 elements a
+// thread and 64 with the sums in memory.
 template <typename T>
 int launch_backward(const NormArgs& a) {
-    constexpr int kVe = 16 / (int)sizeof(T);
-    if (a.c > 32768) {
-        const int parts = row_parts(a.n, 1, kMaxParts);
-        k_rms_norm_backward_long<T><<<parts, kLongThreads, 0, a.stream>>>(
-            static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
-            static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), parts == 1 ? a.dweight : a.part);
-        return parts;
-    }
-    if (a.c % kVe == 0) {
-        constexpr int kE = 32 / (int)sizeof(T);
-        if (a.c <= 4 * kE) return launch_backward_as<T, kVe, 4, kE>(a);
-        if (a.c <= 8 * kE) return launch_backward_as<T, kVe, 8, kE>(a);
-        if (a.c <= 16 * kE) return launch_backward_as<T, kVe, 16, kE>(a);
-        if (a.c <= 32 * kE) return launch_backward_as<T, kVe, 32, kE>(a);
-        if (a.c <= 64 * kE) return launch_backward_as<T, kVe, 64, kE>(a);
-        if (a.c <= 128 * kE) return launch_backward_as<T, kVe, 128, kE>(a);
-        if (a.c <= 256 * kE) return launch_backward_as<T, kVe, 256, kE>(a);
-        if (a.c <= 8192) return launch_backward_as<T, kVe, 512, 16>(a);
-        if (a.c <= 16384) return launch_backward_as<T, kVe, 512, 32>(a);
-        return launch_backward_as<T, kVe, 1024, 32>(a);
-    }
-    return a.c % 2 == 0 ? launch_backward_narrow<T, 2>(a) : launch_backward_narrow<T, 1>(a);
+    constexpr int kE = 32 / (int)sizeof(T);
+    const int span = row_span<T>(a.c);
+    if (span <= 2 * kE) return launch_backward_as<T, 2, kE>(a);
+    if (span <= 4 * kE) return launch_backward_as<T, 4, kE>(a);
+    if (span <= 8 * kE) return launch_backward_as<T, 8, kE>(a);
+    if (span <= 16 * kE) return launch_backward_as<T, 16, kE>(a);
+    if (span <= 32 * kE) return launch_backward_as<T, 32, kE>(a);
+    if (span <= 64 * kE) return launch_backward_as<T, 64, kE>(a);
+    if (span <= 128 * kE) return launch_backward_as<T, 128, kE>(a);
+    if (span <= 256 * kE) return launch_backward_as<T, 256, kE>(a);
+    if (span <= 512 * kE) return launch_backward_as<T, 512, kE>(a);
+    if (span <= 8192) return launch_backward_as<T, 512, 16>(a);
+    if (span <= 16384) return launch_backward_as<T, 1024, 16>(a);
+    const int parts = row_parts(a.n, 1, kMaxParts);
+    k_rms_norm_backward_long<T><<<parts, kLongThreads, 0, a.stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.res), static_cast<const T*>(a.weight), a.rstd_in,
+        static_cast<const T*>(a.dsum), a.n, a.c, static_cast<T*>(a.dx), parts == 1 ? a.dweight : a.part);
+    return parts;
 }
 
 spconv_status_t norm_args(spconv_dtype_t dtype, const void* x, const void* residual, const void* weight, int64_t n,

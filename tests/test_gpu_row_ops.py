@@ -137,7 +137,9 @@ def test_rms_norm_special_rows(sp, c, dtype):
                                  (20, 2048), (17, 2056), (9, 4096), (3, 8192), (5, 8200), (2, 16384), (3, 20001),
                                  (2, 32776), (1, 65536),
                                  # several turns of every CTA
-                                 (60000, 40), (50001, 130), (6000, 515), (3000, 1001), (1700, 4096), (700, 8192), (900, 12000)])
+                                 (60000, 40), (50001, 130), (6000, 515), (3000, 1001), (1700, 4096), (700, 8192), (900, 12000),
+                                 (90001, 17), (80000, 24), (40000, 53), (9000, 163), (4000, 932), (1500, 3333), (900, 4104),
+                                 (1000, 5491), (500, 9001), (4, 2301), (5, 7000)])
 def test_rms_norm_backward(sp, n, c, dtype):
     for weight, dsum in ((True, False), (True, True), (False, True)):
         h, d, w = norm_inputs(n, c, dtype, dsum, weight, seed=9)
@@ -185,6 +187,49 @@ def test_rms_norm_backward_against_autograd_and_differences(sp):
         assert abs(num - float(dx[i, j])) <= 1e-6 + 64 * U * float(mag[i, j])
         num = float(loss(x.double(), w.double() + e[i]) - loss(x.double(), w.double() - e[i])) / 2e-5
         assert abs(num - float(dw[j])) <= 1e-6 + 64 * U * float(magw[j])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,c", [(9, 3), (40, 17), (2001, 36), (700, 57), (700, 61), (301, 125), (301, 130), (150, 250),
+                                 (150, 500), (77, 1018), (5, 2047), (40, 2047), (9, 2301), (30, 4091), (7, 5491),
+                                 (9, 8186), (10, 16381), (6, 32765), (6, 32767)])
+def test_rms_norm_rows_that_start_anywhere(sp, n, c, dtype):
+    """Rows that begin and end inside an item of 16 bytes: every start, first and last rows, and
+    neighbours of infinities and NaN that must not reach the row; nothing is written around them."""
+    x, r, w = norm_inputs(n, c, dtype, True, True, seed=c)
+    x[n // 2] = float("nan")
+    x[n // 3] = float("inf")
+    keep = [i for i in range(n) if i not in (n // 2, n // 3)]
+    y, h, rs = ref.rms_norm(x, w, r, 1e-5)
+    around = torch.full((n * c + 64,), 5.0, dtype=dtype, device="cuda")
+    out = around[32:32 + n * c].view(n, c)
+    sp.spconv_rms_norm(x, w, residual=r, eps=1e-5, out=out)
+    within(out[keep], y[keep], rounding(y[keep], dtype) + chain(c) * U * y[keep].abs())
+    q = torch.full((n * c + 64,), 5.0, device="cuda").to(torch.float8_e4m3fn)
+    s = torch.empty(n, device="cuda")
+    sp.spconv_rms_norm_q8(x, w, residual=r, eps=1e-5, out=q[32:32 + n * c].view(n, c), scale=s)
+    check_q8(q[32:32 + n * c].view(n, c)[keep], s[keep], y[keep], c)
+    # the gradient: a row of NaN and one of infinities stay in their rows of dx
+    dy = randn(n, c, seed=3, dtype=dtype)
+    d = randn(n, c, seed=4, dtype=dtype)
+    hs = x.clone()
+    hs[n // 3] = 1
+    rstd = torch.ones(n, device="cuda")
+    dback = around.clone()
+    dx = dback[32:32 + n * c].view(n, c)
+    for dsum in (None, d):
+        sp.spconv_rms_norm_backward(dy, hs, w, rstd, dsum=dsum, dx=dx)
+        want, _, mag, _ = ref.rms_norm_backward(dy, hs, w, rstd, dsum)
+        rows = [i for i in range(n) if i != n // 2]
+        within(dx[rows], want[rows], rounding(want[rows], dtype) + (chain(c) + 4) * U * mag[rows], "dx")
+        assert dx[n // 2].isnan().all()
+    for buf in (around, dback, q):
+        assert (buf[:32].float() == 5).all() and (buf[32 + n * c:].float() == 5).all()
+    # the weight's gradient over clean rows
+    hs[n // 2] = 1
+    _, dw = sp.spconv_rms_norm_backward(dy, hs, w, rstd)
+    _, wantw, _, magw = ref.rms_norm_backward(dy, hs, w, rstd, None)
+    within(dw, wantw, (n + 8) * U * magw, "dweight")
 
 
 def test_rms_norm_empty(sp):
