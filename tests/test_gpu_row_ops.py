@@ -34,7 +34,8 @@ def within(got, want, tol, what=""):
 
 NORM_SIZES = [(1, 1), (1, 16), (3, 7), (5, 8), (2, 31), (7, 33), (64, 64), (33, 100), (1, 1024), (130, 128), (9, 256),
               (1000, 72), (3, 1000), (4, 2048), (2, 2050), (5, 4096), (3, 4104), (2, 8192), (2, 8200), (1, 16384),
-              (2, 20000), (1, 32776), (1, 40001), (1, 65536), (2, 65535)]
+              (2, 20000), (1, 32776), (1, 40001), (1, 65536), (2, 65535),
+              (70, 24), (31, 80), (9, 90), (33, 144), (17, 320), (9, 700), (7, 696), (2500, 1400), (5, 6001), (3, 12001)]
 
 
 def norm_inputs(n, c, dtype, residual, weight, seed=0):
