@@ -26,7 +26,7 @@ struct MaxNan {
     __device__ static float f(float a, float b) { return max_nan(a, b); }
 };
 
-// The threads of a CTA in groups of TPR, a group a row at a time: 4 to 32 lanes of a
+// The threads of a CTA in groups of TPR, a group a row at a time: 2 to 32 lanes of a
 // warp, or the whole CTA.
 template <int TPR>
 struct Group {
@@ -75,7 +75,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const float* y, float inv
 // thread t at (k * TPR + t) * VE.  One read of x and the residual, one write of each
 // result.  Memory bounds it: with the residual 61,463 x 512 bf16 (and rstd) take 39.5 us,
 // 6.4 TB/s or 97 % of a plain copy's rate, 61,463 x 1024 to 8 bits 67.3 us (100 %), 20,011 x
-// 333 fp32, whose rows start anywhere, 11.3 us (72 %); one row of 1024 channels 2.7 us, most
+// 333 fp32, whose rows start anywhere, 11.5 us (71 %); one row of 1024 channels 2.7 us, most
 // of it the launch.  Branches between items cost a third more (they keep the loads apart),
 // rows fetched ahead through shared memory as in the gradient are no faster.
 template <typename T, int VE, int TPR, int E, bool Q8, bool RES>
