@@ -540,7 +540,8 @@ SPCONV_API spconv_status_t spconv_rms_norm(spconv_dtype_t dtype, const void* x, 
  *   y = h * rstd * weight,  scale = max(max over channels of |y| / 448, 2^-126),
  *   q = y / scale rounded to e4m3 (4 exponent, 3 mantissa bits; nearest even).
  *
- * y is not rounded in between.  A row whose y has a NaN has a NaN scale and NaN codes.
+ * y and the quotient are fp32, each operation rounded to nearest; y is not rounded to
+ * dtype in between.  A row whose y has a NaN has a NaN scale and NaN codes.
  *
  *   q         device bytes [n, channels] (e4m3), scale device fp32 [n].
  */
