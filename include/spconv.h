@@ -596,12 +596,14 @@ typedef struct spconv_rope_s* spconv_rope_t; /* opaque, host memory, owned by th
  * Prepare the turns of a head.
  *
  *   head_dim  even, in [2, SPCONV_ROPE_MAX_HEAD_DIM].
- *   freqs     host double [head_dim / 2], radians per unit of the coordinate, finite.
+ *   freqs     host double [head_dim / 2], radians per unit of the coordinate, under 2^64
+ *             in magnitude.
  *   axes      host int32 [head_dim / 2]: 0, 1 or 2 (columns 1, 2, 3 of coords), or
  *             -1: the pair does not turn.
  *             Both NULL: P = head_dim / 2 / 3 pairs an axis, in the order x, y, z,
  *             with base^(-j / P), j = 0 .. P - 1; the pairs left over do not turn.
- *   base      positive; only read where freqs is NULL.
+ *   base      positive; only read where freqs is NULL.  The frequencies it makes must be
+ *             under 2^64 (a small base makes large ones).
  *   out       receives the handle on success.  It holds no device memory and may be
  *             used on any device and stream.
  */

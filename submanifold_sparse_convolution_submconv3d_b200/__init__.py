@@ -643,7 +643,7 @@ def spconv_rope_create(head_dim: int, layout: str = "interleaved", base: float =
                        axes=None) -> Rope:
     """Rotary positions of heads of ``head_dim`` elements.  ``layout``: "interleaved"
     pairs (2j, 2j + 1), "halves" pairs (j, j + head_dim / 2).  ``freqs`` and ``axes``,
-    sequences of head_dim / 2 numbers, give each pair's radians per unit and its
+    sequences of head_dim / 2 numbers, give each pair's radians per unit (under 2^64) and its
     coordinate (0, 1, 2 = x, y, z; -1 = the pair does not turn); without them every axis
     has head_dim // 6 pairs with the ladder base^(-j / (head_dim // 6))."""
     _require()

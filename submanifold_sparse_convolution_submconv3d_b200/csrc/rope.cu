@@ -5,8 +5,8 @@
 // the gradient is the turn by -t.  The angle is kept in turns, as a 64-bit fixed
 // point fraction: F = freq / (2 pi) mod 1, scaled by 2^64, and F * coord modulo
 // 2^64 is the exact fraction of a turn for any 32-bit coordinate (the error is that
-// of F, 2^-65 times the coordinate), where an fp32 product would be off by 2^-24 of
-// the whole angle: 4e-3 rad at coordinate 65535.
+// of F, which is rounded: 2^-65 of a turn times the coordinate), where an fp32 product
+// would be off by 2^-24 of the whole angle: 4e-3 rad at coordinate 65535.
 #include <math.h>
 
 #include <new>
@@ -202,6 +202,28 @@ void launch_rope(const RopeTable& tab, RopeArgs a, const void* x, void* out, cud
                             st>>>(tab, a, static_cast<const T*>(x), static_cast<T*>(out));
 }
 
+// |freq| under 2^64 as the nearest fraction of a turn in units of 2^-64, modulo a turn: the
+// double's 53 bits times 1 / (2 pi) to 192 bits, in integers, so that no bit of the
+// fraction fades as the frequency grows.
+constexpr double kMaxFreq = 0x1p64;
+uint64_t turn_of(double freq) {
+    static const uint64_t inv_two_pi[3] = {0x36d8a5664f10e410, 0x7f09d5f47d4d3770, 0x28be60db9391054a};  // low word first
+    int e = 0;
+    const uint64_t m = (uint64_t)ldexp(frexp(fabs(freq), &e), 53);
+    const int cut = 128 + 53 - e;  // freq / (2 pi) = m inv_two_pi 2^(e - 53 - 192): bits of the product under 2^-64
+    uint64_t p[5] = {};
+    for (int i = 0; i < 3; ++i) {
+        const unsigned __int128 t = (unsigned __int128)m * inv_two_pi[i] + p[i];
+        p[i] = (uint64_t)t;
+        p[i + 1] = (uint64_t)(t >> 64);
+    }
+    if (cut > 256) return 0;
+    const int word = cut / 64, bit = cut % 64;
+    uint64_t v = bit ? (p[word] >> bit) | (p[word + 1] << (64 - bit)) : p[word];
+    v += (p[(cut - 1) / 64] >> ((cut - 1) % 64)) & 1;
+    return freq < 0.0 ? 0 - v : v;
+}
+
 // 16-byte items where every head starts on a 16-byte boundary and holds whole items,
 // else one pair an item.
 template <typename T>
@@ -245,23 +267,22 @@ spconv_status_t spconv_rope_create(int32_t head_dim, spconv_rope_layout_t layout
     if (!freqs && !(base > 0.0 && base < 1e300))
         return row_fail(SPCONV_ERR_INVALID_ARG, "base must be positive and finite");
     const int pairs = head_dim / 2, per = pairs / 3;
-    if (freqs)
-        for (int j = 0; j < pairs; ++j)
-            if (!(fabs(freqs[j]) < 1e300) || axes[j] < -1 || axes[j] > 2)
-                return row_fail(SPCONV_ERR_INVALID_ARG, "freqs must be finite and axes in [-1, 2]");
+    RopeTable table = {};
+    for (int j = 0; j < pairs; ++j) {
+        const int axis = freqs ? axes[j] : j < 3 * per ? j / per : -1;
+        const double f = freqs ? freqs[j] : axis < 0 ? 0.0 : pow(base, -(double)(j % per) / per);
+        if (!(fabs(f) < kMaxFreq) || axis < -1 || axis > 2)
+            return row_fail(SPCONV_ERR_INVALID_ARG,
+                            freqs ? "freqs must be under 2^64 in magnitude and axes in [-1, 2]"
+                                  : "base makes a frequency of 2^64 or more");
+        table.turn[j] = axis < 0 ? 0 : turn_of(f);
+        table.axis[j] = (int8_t)axis;
+    }
     spconv_rope_s* r = new (std::nothrow) spconv_rope_s();
     if (!r) return row_fail(SPCONV_ERR_OOM, "host allocation failed");
     r->head_dim = head_dim;
     r->layout = layout;
-    const long double two_pi = 6.283185307179586476925286766559005768L;
-    for (int j = 0; j < pairs; ++j) {
-        const int axis = freqs ? axes[j] : j < 3 * per ? j / per : -1;
-        const double f = axis < 0 ? 0.0 : freqs ? freqs[j] : pow(base, -(double)(j % per) / per);
-        long double t = (long double)f / two_pi;
-        t = (t - floorl(t)) * 0x1p64L;
-        r->table.turn[j] = t >= 0x1p64L ? 0 : (uint64_t)t;
-        r->table.axis[j] = (int8_t)axis;
-    }
+    r->table = table;
     *out = r;
     return SPCONV_OK;
 }

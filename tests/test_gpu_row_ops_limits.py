@@ -1,6 +1,9 @@
 """The operators on feature rows (RMS norm, rotary positions, 4-bit linear layer) where a
 last bit, a lost row or a far angle would show: exact results, and bounds counted from the
 launches' own chains of additions."""
+import math
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -79,3 +82,39 @@ def test_q8_codes_of_extreme_scales(sp, c):
         check_codes(sp, 4, c, w)
         w[c // 3] = float("nan")
         check_codes(sp, 4, c, w)
+
+
+# ------------------------------------------------------------------ far angles
+
+PI = Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862089986280348253421170679821, 10 ** 103)
+
+
+def exact_turns(freqs, coords):
+    """cos and sin of freqs[j] * coords[i] in 64 bits, the turn reduced in whole numbers."""
+    t = [[float((Fraction(f) * c / (2 * PI) + Fraction(1, 2)) % 1 - Fraction(1, 2)) for f in freqs] for c in coords]
+    t = torch.tensor(t, dtype=torch.float64, device="cuda") * (2 * math.pi)
+    return t.cos(), t.sin()
+
+
+def turned_units(sp, freqs, coords, dtype):
+    """What a pair (1, 0) becomes: (cos, sin) of every voxel and frequency."""
+    rope = sp.spconv_rope_create(2 * len(freqs), freqs=freqs, axes=[1] * len(freqs))
+    at = torch.zeros((len(coords), 4), dtype=torch.int32, device="cuda")
+    at[:, 2] = torch.tensor(coords, dtype=torch.int32)
+    x = torch.tensor([1.0, 0.0], device="cuda", dtype=dtype).repeat(len(freqs)).expand(len(coords), 1, -1).contiguous()
+    out = sp.spconv_rope_apply(rope, at, x)[:, 0]
+    return out[:, 0::2].double(), out[:, 1::2].double()
+
+
+FAR = [0, 1, -1, 7, 1000, -65535, 123456789, 2 ** 31 - 1, -2 ** 31]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rope_turns_of_any_frequency(sp, dtype):
+    """The fraction of a turn keeps its bits however large the frequency is.  Bound: the
+    cosine and sine of the rounded angle (2^-21 of the pair; bf16 2^-20) and the result's rounding."""
+    freqs = [1.0, 40.0, -40.0, 1e3, 65536.5, 1e9, -1e12, 3e15, 2.0 ** 53 + 2, 1e19, -1.8e19, 2 * math.pi, 1e-9, 2.0 ** -60]
+    freqs += [0.3 * 10.0 ** k for k in range(-4, 14)]
+    tol = (2.0 ** -20 if dtype == BF else 2.0 ** -21) + torch.finfo(dtype).eps / 2
+    for got, want in zip(turned_units(sp, freqs, FAR, dtype), exact_turns(freqs, FAR)):
+        assert float((got - want).abs().max()) <= tol
