@@ -618,7 +618,8 @@ SPCONV_API spconv_status_t spconv_rope_free(spconv_rope_t rope);
  * Turn the heads of n voxels.
  *
  *   coords    device int32 [n, 4], 16-byte aligned; any 32-bit value.  Angles are
- *             exact to 2^-32 of a turn at every coordinate.
+ *             within 2^-32 of a turn at every coordinate; rows of fp32 turn by their sine
+ *             and cosine to the last bits, rows of bf16 by ones within 2^-20.
  *   x         device, aligned to the element: element e of head k of voxel i is at
  *             x[i * x_row + k * x_head + e], so x may be a part of a packed projection.
  *             Strides in elements, in [head_dim, 2^40] (x_row is not read for n = 1,

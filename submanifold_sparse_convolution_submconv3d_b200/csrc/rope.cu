@@ -122,15 +122,20 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
         for (int p = 0; p < kPairs; ++p) {
             const uint32_t ax = (axes >> (2 * p)) & 3u;
             const int c = ax == 1 ? pos.y : ax == 2 ? pos.z : ax == 3 ? pos.w : 0;
-            const int32_t frac = (int32_t)((turn[j0 + p] * (uint64_t)(int64_t)c) >> 32);
+            // the nearest 2^-32 of a turn
+            const int32_t frac = (int32_t)((turn[j0 + p] * (uint64_t)(int64_t)c + (uint64_t(1) << 31)) >> 32);
             if (sizeof(T) == 2) {
                 // 2^-21.2 of error on [-pi, pi], against the 2^-9 of the result's rounding
                 const float ang = (float)frac * 1.46291807926715968e-9f;  // 2 pi / 2^32
                 sn[p] = __sinf(ang) * a.sign;
                 cs[p] = __cosf(ang);
             } else {
-                sincospif((float)frac * 0x1p-31f, &sn[p], &cs[p]);
-                sn[p] *= a.sign;
+                // the 8 bits that fp32 leaves of the fraction turn the sine and cosine a little further
+                const float high = (float)(frac & ~0xff), rest = (float)(frac & 0xff) * 1.46291807926715968e-9f;
+                float sh, ch;
+                sincospif(high * 0x1p-31f, &sh, &ch);
+                sn[p] = fmaf(ch, rest, sh) * a.sign;
+                cs[p] = fmaf(-sh, rest, ch);
             }
         }
         if (kRing) copy_wait<kRopeAhead>();

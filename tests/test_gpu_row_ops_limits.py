@@ -118,3 +118,13 @@ def test_rope_turns_of_any_frequency(sp, dtype):
     tol = (2.0 ** -20 if dtype == BF else 2.0 ** -21) + torch.finfo(dtype).eps / 2
     for got, want in zip(turned_units(sp, freqs, FAR, dtype), exact_turns(freqs, FAR)):
         assert float((got - want).abs().max()) <= tol
+
+
+def test_rope_fp32_angles_are_near_to_the_last_bit(sp):
+    """Angles within 2^-32 of a turn, also where the sine nearly vanishes: 1.5 2^-33 of a turn
+    (2^-34 of the frequency's fraction at coordinate 2^31, 2^-33 of the product's rounding) is
+    under 2^-29 rad; the sine and cosine themselves 2 last bits (2^-22), one operation 2^-24."""
+    freqs = [math.pi * k * (1 + 2.0 ** -m) for m in range(10, 30) for k in (0.25, 0.5, 1.0, 2.0)]
+    freqs += [0.7 ** k for k in range(30)] + [-0.37, 40.0, 1e6]
+    for got, want in zip(turned_units(sp, freqs, FAR, F32), exact_turns(freqs, FAR)):
+        assert ((got - want).abs() <= want.abs() * (2.0 ** -22 + 2.0 ** -24) + 2.0 ** -29).all()
