@@ -623,8 +623,8 @@ SPCONV_API spconv_status_t spconv_rope_free(spconv_rope_t rope);
  *   x         device, aligned to the element: element e of head k of voxel i is at
  *             x[i * x_row + k * x_head + e], so x may be a part of a packed projection.
  *             Strides in elements, in [head_dim, 2^40] (x_row is not read for n = 1,
- *             x_head not for heads = 1).  16-byte aligned buffers whose strides are
- *             multiples of 16 bytes run faster.
+ *             x_head not for heads = 1), n rows at most 2^57 elements.  16-byte aligned
+ *             buffers whose strides are multiples of 16 bytes run faster.
  *   heads     in [1, 4096].
  *   out       as x, with its own strides; rows and heads of out share no elements.
  *             May be x itself with the same strides; must not overlap it otherwise.

@@ -312,6 +312,9 @@ spconv_status_t spconv_rope_apply(spconv_rope_t rope, spconv_dtype_t dtype, cons
     if (x_row < d || out_row < d || x_head < d || out_head < d || x_row > limit || out_row > limit || x_head > limit ||
         out_head > limit)
         return row_fail(SPCONV_ERR_INVALID_ARG, "row and head strides must be in [head_dim, 2^40]");
+    // (so that none of the spans below leaves 64 bits)
+    if (n > 0 && (x_row > (int64_t(1) << 57) / n || out_row > (int64_t(1) << 57) / n))
+        return row_fail(SPCONV_ERR_INVALID_ARG, "n rows must span at most 2^57 elements");
     const int64_t o_in = out_head * (heads - 1) + d, o_rows = out_row * (n > 0 ? n - 1 : 0) + d;
     if (heads > 1 && n > 1 && out_row < o_in && out_head < o_rows)
         return row_fail(SPCONV_ERR_INVALID_ARG, "the strides of out make its rows and heads share elements");

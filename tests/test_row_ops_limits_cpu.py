@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-A, B, C = (0x10000000 * k for k in range(1, 4))  # aligned, far apart
+A, B, C = (1 << k for k in (30, 42, 44))  # aligned, far apart
 
 
 @pytest.fixture(scope="module")
@@ -31,3 +31,20 @@ def test_rope_frequencies_have_a_limit(sp):
     for base in (2.0 ** -71, 1e-5, 0.5, 1.0, 1e299):
         sp.spconv_rope_create(64, base=base).free()
     sp.spconv_rope_create(10, base=5e-324).free()  # one pair an axis: base^0
+
+
+def test_rope_spans_past_64_bits_are_refused(sp):
+    """2^24 steps of 2^40 elements are 2^64: the spans of x and out are not taken modulo that."""
+    handle = ctypes.c_void_p()
+    assert sp.lib.spconv_rope_create(16, 0, 1e4, None, None, ctypes.byref(handle)) == sp.OK
+
+    def apply(n, xr, outr, heads=1, x=B, out=C):
+        return sp.lib.spconv_rope_apply(handle, 1, A, n, x, heads, xr, 16, out, outr, 16, 0, None)
+
+    for n, xr, outr in (((1 << 24) + 1, 16, 1 << 40), ((1 << 24) + 1, 1 << 40, 16), ((1 << 23) + 1, 1 << 40, 1 << 40),
+                        ((1 << 31) - 1, 1 << 32, 1 << 32), ((1 << 24) + 1, 1 << 35, 1 << 35)):
+        assert apply(n, xr, outr) == sp.INVALID_ARG, (n, xr, outr)
+        assert b"2^57" in sp.lib.spconv_last_error()
+        assert apply(n, xr, outr, heads=2) == sp.INVALID_ARG
+    assert apply(0, 1 << 40, 1 << 40) == sp.OK
+    assert sp.lib.spconv_rope_free(handle) == sp.OK
