@@ -7,6 +7,9 @@ from fractions import Fraction
 import pytest
 import torch
 
+import row_ops_bounds as bounds
+from row_ops_bounds import U
+
 pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
@@ -128,3 +131,80 @@ def test_rope_fp32_angles_are_near_to_the_last_bit(sp):
     freqs += [0.7 ** k for k in range(30)] + [-0.37, 40.0, 1e6]
     for got, want in zip(turned_units(sp, freqs, FAR, F32), exact_turns(freqs, FAR)):
         assert ((got - want).abs() <= want.abs() * (2.0 ** -22 + 2.0 ** -24) + 2.0 ** -29).all()
+
+
+# ------------------------------------------------------------------ sums of the norm and its gradient
+
+def within(got, want, tol, what=""):
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:3].tolist())
+
+
+def randn(*shape, seed=0, dtype=F32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n,c", [(70, 8), (70, 16), (70, 31), (70, 64), (70, 96), (70, 128), (33, 190), (33, 256), (33, 384),
+                                 (20, 512), (20, 513), (9, 768), (9, 1024), (2400, 1408), (9, 2048), (5, 2049), (5, 4096),
+                                 (3, 8192), (3, 16383), (2, 32768), (2, 32769), (1, 65536)])
+def test_rms_norm_within_its_own_chain(sp, n, c, dtype):
+    x, r, w = randn(n, c, seed=c, dtype=dtype) * 2, randn(n, c, seed=1, dtype=dtype), (1 + 0.3 * randn(c, seed=2)).to(dtype)
+    rstd = torch.empty(n, device="cuda")
+    out, _ = sp.spconv_rms_norm(x, w, residual=r, eps=1e-6, rstd=rstd)
+    h = x.double() + r.double()
+    want = 1.0 / torch.sqrt((h * h).mean(1) + 1e-6)
+    y = h * want[:, None] * w.double()
+    half = torch.finfo(dtype).eps / 2
+    within(rstd, want, bounds.rstd_bound(c) * want, "rstd")
+    # (the result's rounding, and that of values that only rounding carries over)
+    within(out, y, y.abs() * (half + bounds.norm_bound(c) * (1 + half)), "out")
+    q, s = sp.spconv_rms_norm_q8(x, w, residual=r, eps=1e-6)[:2]
+    top = y.abs().amax(1) / 448
+    within(s, top, (bounds.norm_bound(c) + U) * top, "scale")
+    v = q.double() * s.double()[:, None]
+    within(v, y, torch.maximum(y.abs() * 2.0 ** -4, top[:, None] * 2.0 ** -10) * (1 + 2 * bounds.norm_bound(c)) + y.abs() * 2 * bounds.norm_bound(c), "q")
+
+
+GRADIENTS = [  # one CTA alone, several turns of one, a few CTAs, several turns of all; every count of threads a row
+    (1, 16), (40, 16), (1000, 16), (1025, 16), (2051, 24), (40001, 9), (120000, 32), (70001, 33), (50001, 64), (30001, 120),
+    (17, 256), (40000, 250), (9001, 256), (129, 512), (16, 513), (17, 513), (7001, 500), (5001, 512), (3001, 1024), (5, 2048),
+    (2001, 2047), (1501, 4096), (4, 4096), (901, 4104), (701, 8192), (701, 8191), (303, 12000), (3, 16384), (451, 9001),
+    (300, 16390), (4, 20000), (299, 20001), (700, 33000), (2, 65536)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n,c", GRADIENTS)
+def test_rms_norm_weight_gradient_loses_no_row(sp, n, c, dtype):
+    """Whole numbers under 2^24 in all sums: exact in any order, so one lost or doubled row shows."""
+    g = torch.Generator(device="cuda").manual_seed(n + c)
+    most = 8 if n * 64 < 1 << 24 else 6
+    dy = torch.randint(1, most + 1, (n, c), generator=g, device="cuda").to(dtype)
+    h = torch.randint(1, most + 1, (n, c), generator=g, device="cuda").to(dtype)
+    w = torch.randint(1, 4, (c,), generator=g, device="cuda").to(dtype)
+    want = (dy.double() * h.double()).sum(0)
+    assert float(want.max()) < 2 ** 24
+    for dsum in (None, dy):
+        dx, dw = sp.spconv_rms_norm_backward(dy, h, w, torch.ones(n, device="cuda"), dsum=dsum)
+        assert torch.equal(dw.double(), want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n,c", GRADIENTS)
+def test_rms_norm_gradient_within_its_own_chains(sp, n, c, dtype):
+    h, dy, d = (randn(n, c, seed=c + k, dtype=dtype) for k in range(3))
+    w = (1 + 0.3 * randn(c, seed=3)).to(dtype)
+    rstd = (1 + 0.2 * randn(n, seed=4)).abs() + 0.1
+    hd, dyd, rd = h.double(), dy.double(), rstd.double()[:, None]
+    xh, g = hd * rd, dyd * w.double()
+    mean, meanm = (g * xh).mean(1, keepdim=True), (g * xh).abs().mean(1, keepdim=True)
+    half = torch.finfo(dtype).eps / 2
+    for dsum in (None, d):
+        dx, dw = sp.spconv_rms_norm_backward(dy, h, w, rstd, dsum=dsum)
+        want, mag = rd * (g - xh * mean), rd * (g.abs() + xh.abs() * meanm)
+        if dsum is not None:
+            want, mag = want + dsum.double(), mag + dsum.double().abs()
+        within(dx, want, want.abs() * half + (1 + half) * bounds.dx_bound(c) * mag, "dx")
+        item, per_thread = (4, 8) if dtype == F32 else (8, 16)
+        within(dw, (dyd * xh).sum(0), bounds.column_bound(n, c, item, per_thread) * (dyd * xh).abs().sum(0), "dweight")

@@ -48,3 +48,21 @@ def test_rope_spans_past_64_bits_are_refused(sp):
         assert apply(n, xr, outr, heads=2) == sp.INVALID_ARG
     assert apply(0, 1 << 40, 1 << 40) == sp.OK
     assert sp.lib.spconv_rope_free(handle) == sp.OK
+
+
+def test_column_bound_shows_a_lost_share():
+    """The bound on the weight's gradient is tight enough that the rows of one of 148 CTAs,
+    left out of the 64-bit sums, or a single row, show in most columns
+    (a product 3 a b of two normals is under 0.41, the largest bound here, one time in four)."""
+    import torch
+
+    import row_ops_bounds as bounds
+
+    g = torch.Generator().manual_seed(0)
+    for n, c, item, per_thread in ((90001, 17, 8, 16), (80000, 24, 8, 16), (40000, 53, 4, 8), (50001, 130, 8, 16), (1500, 3333, 4, 8)):
+        terms = torch.randn((n, c), generator=g, dtype=torch.float64) * 3 * torch.randn((n, c), generator=g, dtype=torch.float64)
+        tol = bounds.column_bound(n, c, item, per_thread) * terms.abs().sum(0)
+        rows = bounds.row_groups(c, item, per_thread)
+        cta = (torch.arange(n) // rows) % 148
+        for lost in (cta == 77, torch.arange(n) == 147 * rows):
+            assert (terms[lost].sum(0).abs() > tol).double().mean() > 0.5, (n, c)
