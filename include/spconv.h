@@ -646,7 +646,8 @@ SPCONV_API spconv_status_t spconv_rope_apply(spconv_rope_t rope, spconv_dtype_t 
  * the layout in which the trellis2-mlx-8bit model card's affine groups are stored.
  * group is 32, 64 or 128; cin is a multiple of group, cin and cout at most 2^20.
  *
- * spconv_w4_quantize: from w, device [cin, cout] of dtype, finite.  offset = the
+ * spconv_w4_quantize: from w, device [cin, cout] of dtype, finite, a group's maximum less
+ * its minimum under 2^100 (as spconv_linear_w4 takes the scales to be).  offset = the
  * group's minimum, scale = (maximum - minimum) / 15, both rounded to dtype; q is the
  * nearest code for the rounded pair (0 where the scale is 0).
  */

@@ -532,7 +532,8 @@ def spconv_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, residua
     """Root-mean-square norm of rows x [N, C], with the residual's addition: returns
     ``out``, or ``(out, sum)`` with sum = x + residual where a residual is given.
     ``sum_out`` may be ``residual`` or ``x`` itself; ``rstd``, a float32 CUDA tensor [N],
-    receives what ``spconv_rms_norm_backward`` reads."""
+    receives what ``spconv_rms_norm_backward`` reads.  Inputs that are not contiguous, such
+    as the heads of a packed projection, are copied first."""
     _require()
     index = _norm_rows(x, weight, "x", () if residual is None else (residual,), ("residual",))
     if stream is not None or index != _device_now():
@@ -559,7 +560,8 @@ def spconv_rms_norm_q8(x: torch.Tensor, weight: torch.Tensor | None = None, resi
                        sum_out: torch.Tensor | None = None, stream=None):
     """``spconv_rms_norm`` with the result in 8 bits: returns ``(q, scale)`` or ``(q,
     scale, sum)``, q float8_e4m3fn [N, C] and scale float32 [N], the norm being about
-    q * scale."""
+    q * scale.  ``spconv_linear_w4`` takes both, for up to W4_MAX_ROWS rows; the layers for
+    more rows take float32 and bfloat16, as ``spconv_rms_norm`` writes them."""
     _require()
     index = _norm_rows(x, weight, "x", () if residual is None else (residual,), ("residual",))
     if stream is not None or index != _device_now():

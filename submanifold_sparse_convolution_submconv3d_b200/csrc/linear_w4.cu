@@ -51,7 +51,7 @@ __device__ __forceinline__ void mma_tile(float (&d)[4], const uint32_t (&a)[4], 
 // in the lowest places are q 2^-24, four places up 16 q 2^-24, so a code needs one mask
 // (and every other pair a shift); the pairs four places up meet x / 16, which fp16 holds.
 // (The same in e4m3's own steps of 32 channels would take fewer masks, but those steps run
-// as conversions and two fp16 steps: 19.4 us against 17.6 for 8 rows through 8192 x 16384.)
+// as conversions and two fp16 steps: a tenth slower for 8 rows through 8192 x 16384.)
 template <typename X>
 struct Codes {
     using Elem = __half;
@@ -188,16 +188,23 @@ struct W4Params {
 // into shared memory (a lane copies for its own output alone, so no warp waits for
 // another) and the next chunk's x into registers.
 //
-// What bounds it.  8 e4m3 rows through 8192 x 16384, groups of 128, take 17.6 us, 4.1 TB/s
-// of codes and scales or 62 % of a plain copy's rate; bf16 rows 23.7 us, with groups of 64
-// 25 us.  There the integer pipe is busiest (60 %): making operands of the codes (7
-// instructions a word of 8) is 5 us and the scales are 2.4 us of it, measured by leaving
-// them out.  More rows bring more steps and scaled sums a code: 16 bf16 rows 29.9 us, 32
-// rows through 4096 x 16384 27.3 us.  One row through 4096 x 4096: 6.2 us.  Fewer tiles a
+// What bounds it.  8 e4m3 rows through 8192 x 16384, groups of 128, take 16.9 us, 4.2 TB/s
+// of codes and scales or 65 % of a plain copy's rate; bf16 rows 22.3 us, with groups of 64
+// 24.3 us.  No unit is full: the integer pipe is busiest (49 %, for 16 bf16 rows 50 %), the
+// tensor pipe has 28 (32) %, half of the issue slots are used.  One CTA of 16 warps an SM
+// spends 21 % of its time before the first step (first scales and codes on their way), 70 %
+// in the steps and 8 % in the join (7,100, 23,200 and 2,600 of 33,000 cycles, measured by
+// stamps), and in the steps its warps wait for their own chains of them.  For bf16 making
+// operands of the codes (7 instructions a word of 8) is 5 us and the scales are 2.4 us,
+// measured by leaving them out.  More rows bring more steps and scaled sums a code: 16 bf16
+// rows 29.5 us, 32 rows through 4096 x 16384 27.0 us.  One row through 4096 x 4096: 5.7 us,
+// 27 % of a CTA's time before the first step, 65 % in four steps a warp, 8 % in the join.  Fewer tiles a
 // CTA (two: 43 us for 8 bf16 rows), and a warp that holds codes and reads x anew for every
 // tile (44 us), are slower.  The steps are the 16-channel ones that take operands from
-// registers: tcgen05 takes them from shared memory, where the operands would be written
-// at four times the codes' size, and its sums would have to be read back for each group.
+// registers.  tcgen05 would take the codes' operands from tensor or shared memory, so that
+// the threads that make them would also write them there, at four times the codes' size, and
+// it would save the tensor steps' issue alone, which is not what bounds it; and the sums of
+// each group would have to be read back from tensor memory before its scales.
 //
 // Fragments.  In one 16 x 8 x 16 step lane (g, t) = (lane / 4, lane % 4) holds four
 // input channels of outputs g and g + 8 and of row g; which four is free as long as both

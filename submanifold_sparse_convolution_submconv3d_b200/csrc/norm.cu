@@ -59,8 +59,8 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
 
 // y / s rounded once to fp32, for s with the reciprocal `inv`: the product y inv is off by a
 // last bit now and then, so that a value next to the middle of two codes falls to the other
-// one; the remainder y - s (y inv), exact in one fused operation, mends it (P. W. Markstein,
-// IBM J. Res. Dev. 34, 1990).  210,354 x 128 bf16 to 8 bits take 19.0 us, with the product alone
+// one; the remainder y - s (y inv), exact in one fused operation down to |y| = 2^-102, mends
+// it (P. W. Markstein, IBM J. Res. Dev. 34, 1990).  210,354 x 128 bf16 to 8 bits take 19.0 us, with the product alone
 // 17.9 and with the division of every value 24.3.  back = -s, or 0 where s is infinite: then
 // inv = 0 and the quotients of finite values are 0.
 __device__ __forceinline__ float quotient(float y, float back, float inv) {
@@ -602,11 +602,15 @@ void launch_forward_narrow(const NormArgs& a) {
     else launch_forward_as<T, VE, 1024, 32, Q8>(a);
 }
 
-// A thread holds up to 32 elements of a row; the fewest threads that hold it take it, so
-// that a row's sums cross few threads and the rows in work, one a group, are many: 210,354 x
-// 80 bf16 to 8 bits take 13.9 us with 4 threads a row, 18.2 with 8 and 22.4 with 16.  Many
-// rows of up to 1536 channels to 8 bits, which join their threads twice, stay in a warp:
-// 16,862 x 1408 bf16 18.9 us, 24.0 with 128 threads a row; few rows are 1 us slower so.
+// A thread holds up to 32 elements of a row, and few threads take it, so that a row's sums
+// cross few threads and the rows in work, one a group, are many: 210,354 x 80 bf16 to 8 bits
+// take 14.4 us with 4 threads a row, 19.5 with 8 and 24.6 with 16.  Two lengths have twice the
+// threads that hold the row: up to 64 channels (300,000 x 64 bf16 with a residual 24.7 us,
+// with 2 threads 27.7; to 8 bits 15.2 and 14.8) and up to 512 (61,463 x 512 with a residual
+// 39.2 us, with 16 threads 39.7; to 8 bits 34.9 and 35.8, without a residual 23.1 and 21.6).
+// Above a warp a row has the whole CTA of 128 threads or more.  Many rows of up to 1536
+// channels to 8 bits, which join their threads twice, stay in a warp of 48 elements a lane:
+// 16,862 x 1408 bf16 19.6 us, 24.8 with 128 threads a row; few rows are 1 us slower so.
 template <typename T, bool Q8>
 void launch_forward(const NormArgs& a) {
     constexpr int kVe = 16 / (int)sizeof(T);
@@ -678,9 +682,11 @@ int row_span(int c) {
 }
 
 // 32 bytes of a row a thread (bf16: 16 elements, fp32: 8), as many threads as that takes; 16
-// bytes a thread and twice the threads are a quarter to a half slower.  From 16,384 channels on
-// the columns' sums do not fit the registers: 900 x 20,000 bf16 take 97 us with 32 elements a
-// thread and 64 with the sums in memory.
+// bytes a thread and twice the threads are a quarter to a half slower.  From 8,193 channels on
+// 16 elements for each of 1024 threads do not fit the 64 registers that a thread then has:
+// 180 to 850 bytes a thread go through local memory, 900 x 12,000 bf16 take 32 us, 31 % of a
+// copy's rate.  Above 16,384 channels the
+// columns' sums are in memory: 900 x 20,000 bf16 66 us, 97 with 32 elements a thread.
 template <typename T>
 int launch_backward(const NormArgs& a) {
     constexpr int kE = 32 / (int)sizeof(T);

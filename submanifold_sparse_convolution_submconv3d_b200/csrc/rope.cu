@@ -61,7 +61,10 @@ constexpr int kRopeSmem = kWide<T, VE> ? (kRopeAhead + 1) * 4 * 16 * kRopeThread
 // Memory bounds it: 273,995 voxels of 12 x 64 in bf16, out of a packed projection, take
 // 136 us, 6.2 TB/s or 95 % of a plain copy's rate; 16,934 of 8 x 96 in fp32 halves 20 us
 // (80 %: a head's 12 items leave 8 lanes of a warp idle, and fp32 sines are long); one
-// voxel 2.7 us.  One pair a thread with a sine each took 1,717 us for the first.
+// voxel 2.3 us.  One pair a thread with a sine each took 1,717 us for the first.  Items of
+// one pair, for heads that are no whole number of 16-byte items, are not fetched ahead and wait
+// for their loads: 100,000 voxels of 8 x 72 in bf16 halves 167 us (21 %), of 8 x 36
+// interleaved 73 us (24 %).
 template <typename T, int VE, bool HALVES>
 __global__ void __launch_bounds__(kRopeThreads, 4)
     k_rope(const __grid_constant__ RopeTable tab, const __grid_constant__ RopeArgs a, const T* x, T* out) {
